@@ -520,6 +520,171 @@ SELSCAN_API int selscan_ssd_fwd(const void *x, const void *dt, const float *A, c
 SELSCAN_API int64_t selscan_ssd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
                                                 int64_t headdim, int64_t dstate);
 
+/* Options of selscan_linattn_fwd and selscan_linattn_bwd; zero-initialised (or
+ * NULL): no decay, a zero first state, every token of every row, contiguous
+ * operands. At most one of the two decays is given (else SELSCAN_ERR_BAD_DIM). */
+typedef struct {
+    const void *log_decay;       /* [batch, seqlen, heads] dtype: g of every token */
+    const float *head_log_decay; /* [heads]: one g for all tokens of a head */
+    const float *initial_state;  /* [batch, heads, dk, dv]: S before token 0 */
+    const int32_t *seqlens;      /* [batch], on the device: tokens of each row (clamped to
+                                    0..seqlen); NULL -> seqlen */
+    int64_t q_stride, k_stride, v_stride; /* elements between tokens; 0 -> contiguous.
+                                    A row's heads are contiguous, batch rows seqlen tokens
+                                    apart: q, k and v may be slices of one projection */
+} selscan_linattn_options_t;
+
+/*
+ * selscan_linattn_fwd -- linear attention with a decay for each head: the
+ * matrix form of "Mamba & State Space Models — Guide Complet" §5 ("SSD — State
+ * Space Dual") with a query and a key of their own for each head (or shared by
+ * heads/qk_heads neighbouring heads) and free log decays. Per (batch row, head):
+ *   S_t = exp(g_t)·S_{t−1} + k_t v_tᵀ,    y_t = scale·S_tᵀ q_t
+ *   q, k          [batch, seqlen, qk_heads, dk]   dtype     required
+ *   v, y          [batch, seqlen, heads, dv]      dtype     required (y: output)
+ *   final_state   [batch, heads, dk, dv]          float32   NULL -> not written; may be
+ *                                                 options->initial_state itself
+ *   heads a multiple of qk_heads, 1 <= dk, dv <= 128, batch·heads <= 2^22.
+ * A log decay of −∞ (any below −111) resets: what came before that token does
+ * not count. Tokens at or behind a row's length are not used: their y is zero
+ * and final_state is the state after the row's last token; their k and v may
+ * hold anything. Chunks of 64 tokens; float32 state, sums and decays. bfloat16
+ * I/O whose rows suit it (dk, dv multiples of 8, 16-byte rows) runs on the
+ * tensor cores (tcgen05) with the products' weights and the entering state as
+ * bfloat16 operands, the state's own update keeping 24 bits; everything else
+ * in float32 on the CUDA cores. Few (batch row, head) pairs: a sequence is cut
+ * into segments that run side by side after a pass over their own states.
+ * Workspace (256-byte aligned; NULL: allocated on the stream) of
+ * selscan_linattn_workspace_bytes() bytes. Results do not depend on anything
+ * but the inputs (fixed summation order). Asynchronous like selscan_fwd.
+ */
+SELSCAN_API int selscan_linattn_fwd(const void *q, const void *k, const void *v, float scale,
+                                    const selscan_linattn_options_t *options, void *y,
+                                    float *final_state, int64_t batch, int64_t seqlen,
+                                    int64_t qk_heads, int64_t heads, int64_t dk, int64_t dv,
+                                    selscan_dtype_t dtype, void *workspace,
+                                    int64_t workspace_bytes, selscan_stream_t stream);
+
+/* Host-only: workspace bytes selscan_linattn_fwd takes (0 for empty or invalid sizes). */
+SELSCAN_API int64_t selscan_linattn_workspace_bytes(int64_t batch, int64_t seqlen,
+                                                    int64_t qk_heads, int64_t heads, int64_t dk,
+                                                    int64_t dv, selscan_dtype_t dtype);
+
+/*
+ * selscan_linattn_bwd -- the gradient of selscan_linattn_fwd for the loss
+ * Σ dy·y + Σ dfinal_state·final_state. With N_t = ∂loss/∂S_t (N after the last
+ * token = dfinal_state), N_t = scale·q_t dy_tᵀ + exp(g_{t+1})·N_{t+1}:
+ *   dq_t = scale·S_t dy_t, dk_t = N_t v_t, dv_t = N_tᵀ k_t (sums over the heads
+ *   that share a q and a k), dg_t = exp(g_t)·<S_{t−1}, N_t>
+ *   dy             [batch, seqlen, heads, dv]     dtype     required
+ *   dfinal_state   [batch, heads, dk, dv]         float32   NULL -> zero
+ *   dq, dk         [batch, seqlen, qk_heads, dk]  dtype     required outputs
+ *   dv             [batch, seqlen, heads, dv]     dtype     required output
+ *   dlog_decay     [batch, seqlen, heads]         dtype     NULL -> not written;
+ *                                                 needs options->log_decay (a decay
+ *                                                 given by head is a constant)
+ *   dinitial_state [batch, heads, dk, dv]         float32   NULL -> not written
+ * States are recomputed. Every output is overwritten; those of tokens behind a
+ * row's length are zero. Options, limits and workspace
+ * (selscan_linattn_bwd_workspace_bytes()) as for the forward. Outputs are
+ * contiguous and overlap no input.
+ */
+SELSCAN_API int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale,
+                                    const selscan_linattn_options_t *options, const void *dy,
+                                    const float *dfinal_state, void *dq, void *dk_out,
+                                    void *dv_out, void *dlog_decay, float *dinitial_state,
+                                    int64_t batch, int64_t seqlen, int64_t qk_heads,
+                                    int64_t heads, int64_t dk, int64_t dv, selscan_dtype_t dtype,
+                                    void *workspace, int64_t workspace_bytes,
+                                    selscan_stream_t stream);
+
+/* Host-only: workspace bytes selscan_linattn_bwd takes (0 for empty or invalid sizes). */
+SELSCAN_API int64_t selscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen,
+                                                        int64_t qk_heads, int64_t heads,
+                                                        int64_t dk, int64_t dv,
+                                                        selscan_dtype_t dtype);
+
+/*
+ * selscan_linattn_step -- one token of selscan_linattn_fwd, the state updated
+ * in place (recurrent inference after a prompt's final_state):
+ *   state       [batch, heads, dk, dv]   float32   read and overwritten
+ *   q, k        [batch, qk_heads, dk]    dtype     required
+ *   v, y        [batch, heads, dv]       dtype     required (y: output)
+ *   log_decay   [batch, heads] dtype, or head_log_decay [heads] float32, or
+ *               neither (no decay); both: SELSCAN_ERR_BAD_DIM
+ * A log decay of −∞ resets the state (its old content does not count). No
+ * memory is allocated.
+ */
+SELSCAN_API int selscan_linattn_step(float *state, const void *q, const void *k, const void *v,
+                                     const void *log_decay, const float *head_log_decay,
+                                     float scale, void *y, int64_t batch, int64_t qk_heads,
+                                     int64_t heads, int64_t dk, int64_t dv, selscan_dtype_t dtype,
+                                     selscan_stream_t stream);
+
+/* Where the gate silu(z) of selscan_block_norm_fwd stands. */
+enum {
+    SELSCAN_GATE_NONE = 0,
+    SELSCAN_GATE_BEFORE = 1, /* the block's output is gated, then normed */
+    SELSCAN_GATE_AFTER = 2   /* normed, then gated */
+};
+
+/* Options of selscan_block_norm_fwd and selscan_block_norm_bwd. */
+typedef struct {
+    const void *z;            /* [rows, dim] dtype (gate != SELSCAN_GATE_NONE) */
+    int64_t x_stride, z_stride; /* elements between rows; 0 -> dim */
+    const float *weight;      /* [dim]: the norm after the block; NULL -> no such norm */
+    const void *residual;     /* [rows, dim]; NULL -> none */
+    const float *res_scale;   /* [dim]: scale of the block's branch; NULL -> one */
+    const float *next_weight; /* [dim]: the norm before the next block; NULL -> none */
+    int64_t groups;           /* groups of the norm after the block (0 -> 1; needs weight when
+                                 above 1; divides dim; up to 1024) */
+    int gate;                 /* SELSCAN_GATE_* */
+    int residual_f32;         /* residual, out, dout and dresidual are float32 whatever dtype is */
+    float eps;                /* >= 0 */
+} selscan_block_norm_options_t;
+
+/*
+ * selscan_block_norm_fwd -- what stands between two blocks, in one pass: the
+ * norm of the block's output with its gate ("Mamba Block": y·silu(z)), the
+ * scaled residual sum, and the norm before the next block. Per row:
+ *   a   = x                (SELSCAN_GATE_BEFORE: x·silu(z))
+ *   p   = a·rsqrt(mean_group(a²) + eps)·weight     (weight NULL: p = a)
+ *   u   = p                (SELSCAN_GATE_AFTER: p·silu(z))
+ *   out = residual + res_scale·u
+ *   y   = out·rsqrt(mean(out²) + eps)·next_weight  (from the unrounded out)
+ *   x, y   [rows, dim]   dtype            x required; y required iff next_weight is given
+ *   out    [rows, dim]   residual's type  NULL -> not written (then y is); may be
+ *                                         residual itself
+ *   1 <= dim <= 16384, rows < 2^31. Arithmetic and sums are float32.
+ */
+SELSCAN_API int selscan_block_norm_fwd(const void *x, const selscan_block_norm_options_t *options,
+                                       void *out, void *y, int64_t rows, int64_t dim,
+                                       selscan_dtype_t dtype, selscan_stream_t stream);
+
+/*
+ * selscan_block_norm_bwd -- the gradient of selscan_block_norm_fwd for the loss
+ * Σ dout·out + Σ dy·y, everything of the forward recomputed from its inputs:
+ *   dout       [rows, dim]  residual's type  NULL -> zero (then dy is given)
+ *   dy         [rows, dim]  dtype            required iff next_weight is given
+ *   dx         [rows, dim]  dtype            required output
+ *   dz         [rows, dim]  dtype            required output with a gate
+ *   dresidual  [rows, dim]  residual's type  NULL -> not written
+ *   dweight, dres_scale, dnext_weight [dim] float32, sums over the rows in a
+ *              fixed order; NULL -> not written
+ * Outputs are contiguous, overwritten, and overlap no input. Workspace
+ * (256-byte aligned; NULL: allocated on the stream) of
+ * selscan_block_norm_bwd_workspace_bytes() bytes.
+ */
+SELSCAN_API int selscan_block_norm_bwd(const void *x, const selscan_block_norm_options_t *options,
+                                       const void *dout, const void *dy, void *dx, void *dz,
+                                       void *dresidual, float *dweight, float *dres_scale,
+                                       float *dnext_weight, int64_t rows, int64_t dim,
+                                       selscan_dtype_t dtype, void *workspace,
+                                       int64_t workspace_bytes, selscan_stream_t stream);
+
+/* Host-only: workspace bytes selscan_block_norm_bwd takes (0 for empty or invalid sizes). */
+SELSCAN_API int64_t selscan_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
 /*
  * selscan_device_status -- the library's sticky device-side error word on
  * the current device (synchronous: waits for prior work). 0 means no device

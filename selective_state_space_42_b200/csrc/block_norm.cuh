@@ -1,0 +1,34 @@
+// block_norm.cuh -- launch parameters and entry points of the block-norm
+// junction and its gradient (block_norm.cu).
+#pragma once
+
+#include "selscan_device.cuh"
+
+namespace selscan {
+
+constexpr int kBnMaxDim = 16384;
+constexpr int kBnMaxGroups = 1024;
+enum { kGateNone = 0, kGateBefore = 1, kGateAfter = 2 };
+
+struct BlockNormParams {
+    const void *x, *z;                  // rows of dim elements, x_row / z_row apart
+    long long x_row, z_row;
+    const float *weight, *res_scale, *next_weight;  // [dim] or NULL
+    const void *res;                    // [rows][dim] or NULL
+    void *out, *y;                      // forward: [rows][dim], each may be NULL
+    const void *dout, *dy;              // gradient: [rows][dim], each may be NULL
+    void *dx, *dz, *dres;
+    float *partial;                     // [slots][3][dim]: dweight, dres_scale, dnext_weight sums
+    float *dweight, *dres_scale, *dnext_weight;
+    long long rows;
+    int dim, groups;
+    int gate;
+    int res_f32;                        // type of res, out, dout, dres (else the I/O type)
+    int vec;                            // every row starts on a 16-byte boundary
+    float eps;
+};
+cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
+cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
+int block_norm_bwd_slots(long long rows, int dim);  // sizes `partial`
+
+}  // namespace selscan

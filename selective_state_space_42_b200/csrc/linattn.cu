@@ -1,0 +1,618 @@
+// linattn.cu -- linear attention with a decay for each head on the CUDA cores:
+// the sweep of linattn_params.cuh in chunks of 64 tokens, for every size and
+// alignment and both I/O types, with float32 products (the float32 I/O path;
+// bfloat16 I/O comes here only when its rows do not suit the tensor-core
+// kernels).
+//
+// With within-chunk prefix sums G_i of the log decays (G_end their total), a
+// chunk's outputs and state are dense products ("Mamba & State Space Models —
+// Guide Complet" §5 "SSD — State Space Dual", with a key and a query of their
+// own for each head):
+//   forward:  y_i  = Σ_{j ≤ i} p·exp(G_i − G_j)·(q_i·k_j)·v_j + r·exp(G_i)·S_inᵀ q_i
+//             S_out = exp(G_end)·S_in + Σ_j c·exp(G_end − G_j)·k_j v_jᵀ
+//   reverse:  y_j  = Σ_{i ≥ j} p·exp(G_i − G_j)·(q_j·k_i)·v_i + r·exp(G_end − G_j)·S_inᵀ q_j
+//             S_out = exp(G_end)·S_in + Σ_i c·exp(G_i)·k_i v_iᵀ
+// A block carries the state of one head and 64 of its value columns through
+// the chunks of one segment, in registers (with a shared-memory copy for the
+// product with q). Too few heads to fill the device: the sequence is cut into
+// segments; a first pass finds each segment's own state, a carry over the
+// segments turns them into the states entering, and all segments run at once.
+//
+// Bound: the float32 FMA rate; per chunk 2·64·64·(dk + dv) + 2·2·64·dk·dv
+// operations a head, which the products' register tiles (4×4, and
+// (dk/16)×4 for the state) feed from shared memory.
+#include "linattn_params.cuh"
+
+#include <algorithm>
+
+namespace selscan {
+namespace {
+
+constexpr int kC = kLaChunk;
+constexpr int kVt = 64;        // value columns per block
+constexpr int kThr = 256;
+constexpr int kLd = kC + 4;    // row stride of the token-minor tiles (keeps 16-byte rows, spreads banks)
+
+template <int DKP> struct SweepSmem {
+    float Q[DKP][kLd];   // [d][token]
+    float K[DKP][kLd];
+    float V[kC][kVt];    // [token][column]
+    float P[kC][kLd];    // [col token][row token]
+    float S[DKP][kVt];   // the state entering the chunk
+    float gh[kC], gl[kC];        // prefix sums times log2(e), as high + low
+    float rowf[kC], colw[kC];
+    float decay;
+    float decay_log2_h, decay_log2_l;
+};
+
+// Four consecutive elements from `c` of a row with `n` valid ones, zero past them.
+template <typename T>
+__device__ __forceinline__ float4 ld4(const T *row, int c, int n, bool vec);
+template <>
+__device__ __forceinline__ float4 ld4<float>(const float *row, int c, int n, bool vec) {
+    if (vec && c + 4 <= n) return __ldg(reinterpret_cast<const float4 *>(row + c));
+    float4 v;
+    v.x = c < n ? __ldg(row + c) : 0.f;
+    v.y = c + 1 < n ? __ldg(row + c + 1) : 0.f;
+    v.z = c + 2 < n ? __ldg(row + c + 2) : 0.f;
+    v.w = c + 3 < n ? __ldg(row + c + 3) : 0.f;
+    return v;
+}
+template <>
+__device__ __forceinline__ float4 ld4<__nv_bfloat16>(const __nv_bfloat16 *row, int c, int n,
+                                                     bool vec) {
+    if (vec && c + 4 <= n) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(row + c));
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+    }
+    float4 v;
+    v.x = c < n ? ldg_f32(row + c) : 0.f;
+    v.y = c + 1 < n ? ldg_f32(row + c + 1) : 0.f;
+    v.z = c + 2 < n ? ldg_f32(row + c + 2) : 0.f;
+    v.w = c + 3 < n ? ldg_f32(row + c + 3) : 0.f;
+    return v;
+}
+
+__device__ __forceinline__ void st4(float *p, const float4 &v) {
+    *reinterpret_cast<float4 *>(p) = v;
+}
+__device__ __forceinline__ void st4(__nv_bfloat16 *p, const float4 &v) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                               *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// A [nq tokens][n columns] tile into shared memory as [column][token], zero
+// outside. Lanes run over tokens, so that the transposed stores hit distinct
+// banks; the four elements a lane reads per step share a sector with its
+// next step's.
+template <typename T, int DKP>
+__device__ __forceinline__ void load_transposed(float (*dst)[kLd], const T *base, long long row,
+                                                int nq, int n, bool vec) {
+    const int tok = threadIdx.x & (kC - 1), grp = threadIdx.x / kC;
+    const T *r = base + tok * row;
+#pragma unroll
+    for (int it = 0; it < DKP / 16; ++it) {
+        const int d = 4 * (grp + 4 * it);
+        const float4 v = tok < nq ? ld4<T>(r, d, n, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        dst[d][tok] = v.x;
+        dst[d + 1][tok] = v.y;
+        dst[d + 2][tok] = v.z;
+        dst[d + 3][tok] = v.w;
+    }
+}
+
+__device__ __forceinline__ void fma4(float4 &a, float s, const float4 &b) {
+    a.x = fmaf(s, b.x, a.x);
+    a.y = fmaf(s, b.y, a.y);
+    a.z = fmaf(s, b.z, a.z);
+    a.w = fmaf(s, b.w, a.w);
+}
+
+// Prefix sums of the chunk's log decays (one warp, two tokens a lane, in
+// double: 64 tokens of strong decay would otherwise leave float32 too few
+// bits for the difference of two neighbours) and the factors made from them.
+template <typename T>
+__device__ __forceinline__ void chunk_decays(const LinattnParams &p, const SweepArgs &a,
+                                             long long b, int h, long long t0, int nq, float *gh,
+                                             float *gl, float *rowf, float *colw, float *decay,
+                                             float *total_h, float *total_l) {
+    const int lane = threadIdx.x;
+    double s[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int t = 2 * lane + e;
+        double g = 0.0;
+        if (t < nq) {
+            if (p.g)
+                g = (double)ldg_f32(static_cast<const T *>(p.g) +
+                                    (b * p.seqlen + t0 + t) * p.heads + h);
+            else if (p.g_head)
+                g = (double)__ldg(p.g_head + h);
+            g *= 1.4426950408889634;
+            g = g < kLaResetLog2 ? kLaResetLog2 : g;
+        }
+        s[e] = g;
+    }
+    double sum = s[0] + s[1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, sum, m);
+        if (lane >= m) sum += o;
+    }
+    const double end = __shfl_sync(0xffffffffu, sum, 31);
+    const double G[2] = {sum - s[1], sum};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int t = 2 * lane + e;
+        const float hi = (float)G[e];
+        gh[t] = hi;
+        gl[t] = (float)(G[e] - (double)hi);
+        const float up = ex2_approx((float)G[e]), down = ex2_approx((float)(end - G[e]));
+        rowf[t] = a.row_scale * (a.reverse ? down : up);
+        colw[t] = a.col_scale * (a.reverse ? up : down);
+    }
+    if (lane == 0) {
+        *decay = ex2_approx((float)end);
+        *total_h = (float)end;
+        *total_l = (float)(end - (double)(float)end);
+    }
+}
+
+// One block: one (sweep, batch row, head, segment, 64 value columns).
+// kFull false: only the segment's own state, from zero.
+template <typename T, int DKP, bool kFull>
+__global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const LinattnParams p) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SweepSmem<DKP> &S = *reinterpret_cast<SweepSmem<DKP> *>(smem_raw);
+    const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
+    constexpr int kTiles = DKP / kVt;
+    long long id = blockIdx.x;
+    const int tile = (int)(id % kTiles);
+    id /= kTiles;
+    const int order = (int)(id % nruns);  // position in the sweep's direction
+    id /= nruns;
+    const int sw = (int)(id % p.nsweeps);
+    const long long bh = id / p.nsweeps;
+    const SweepArgs &a = p.sweep[sw];
+    const int v0 = tile * kVt;
+    if (v0 >= a.dv) return;
+    const long long b = bh / p.heads;
+    const int h = (int)(bh % p.heads);
+    const int seg = a.reverse ? p.nseg - 1 - order : order;
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    const long long len = p.seqlens
+                              ? min((long long)max(__ldg(p.seqlens + b), 0), p.seqlen)
+                              : p.seqlen;
+    const long long row0 = b * p.seqlen;
+    const T *Q = static_cast<const T *>(a.q) + row0 * a.q_row + (long long)(h / a.q_group) * a.dk;
+    const T *K = static_cast<const T *>(a.k) + row0 * a.k_row + (long long)(h / a.k_group) * a.dk;
+    const T *V = static_cast<const T *>(a.v) + row0 * a.v_row + (long long)(h / a.v_group) * a.dv;
+    const bool vec = p.vec != 0;
+    const long long state_elems = (long long)a.dk * a.dv;
+
+    // the state: rows d = ty + 16·r, columns v0 + 4·tx .. + 3
+    constexpr int kR = DKP / 16;
+    float4 st[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int d = ty + 16 * r;
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+        if (kFull && d < a.dk) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int v = v0 + 4 * tx + c;
+                if (v >= a.dv) continue;
+                if (p.nseg > 1)
+                    e[c] = a.seg_state[(bh * p.nseg + seg) * state_elems + (long long)d * a.dv + v];
+                else if (a.h_init)
+                    e[c] = a.h_init[bh * state_elems + (a.h_init_t ? (long long)v * a.dk + d
+                                                                   : (long long)d * a.dv + v)];
+            }
+        }
+        st[r] = make_float4(e[0], e[1], e[2], e[3]);
+    }
+    double seg_log2 = 0.0;  // of the segment's decay (thread 0)
+
+    const int c_first = seg * p.seg_chunks;
+    const int c_last = min(p.nchunks, c_first + p.seg_chunks);
+    for (int i = 0; i < c_last - c_first; ++i) {
+        const int c = a.reverse ? c_last - 1 - i : c_first + i;
+        const long long t0 = (long long)c * kC;
+        const int nq = (int)max(0ll, min((long long)kC, len - t0));
+        const int nl = (int)min((long long)kC, p.seqlen - t0);
+        if (nq == 0 && !kFull) continue;
+        __syncthreads();  // the tiles' readers of the previous chunk are done
+        if (nq > 0) {
+            if (kFull) load_transposed<T, DKP>(S.Q, Q + t0 * a.q_row, a.q_row, nq, a.dk, vec);
+            load_transposed<T, DKP>(S.K, K + t0 * a.k_row, a.k_row, nq, a.dk, vec);
+#pragma unroll
+            for (int k = 0; k < kC * kVt / 4 / kThr; ++k) {
+                const int it = t + k * kThr, tok = it / (kVt / 4), c4 = 4 * (it % (kVt / 4));
+                *reinterpret_cast<float4 *>(&S.V[tok][c4]) =
+                    tok < nq ? ld4<T>(V + (t0 + tok) * a.v_row, v0 + c4, a.dv, vec)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (kFull) {
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+                    *reinterpret_cast<float4 *>(&S.S[ty + 16 * r][4 * tx]) = st[r];
+            }
+            if (t < 32)
+                chunk_decays<T>(p, a, b, h, t0, nq, S.gh, S.gl, S.rowf, S.colw, &S.decay,
+                                &S.decay_log2_h, &S.decay_log2_l);
+        }
+        __syncthreads();
+        float4 acc[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (nq > 0) {
+            if (kFull) {
+                // P[row 4·ty + r][col 4·tx + c]
+#pragma unroll 4
+                for (int d = 0; d < a.dk; ++d) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(&S.Q[d][4 * ty]);
+                    const float4 k4 = *reinterpret_cast<const float4 *>(&S.K[d][4 * tx]);
+                    fma4(acc[0], q4.x, k4);
+                    fma4(acc[1], q4.y, k4);
+                    fma4(acc[2], q4.z, k4);
+                    fma4(acc[3], q4.w, k4);
+                }
+                float w[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i0 = 4 * ty + r;
+                    const float *av = reinterpret_cast<const float *>(&acc[r]);
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) {
+                        const int j0 = 4 * tx + cc;
+                        const bool in = (a.reverse ? j0 >= i0 : j0 <= i0) && i0 < nq && j0 < nq;
+                        float d = (S.gh[i0] - S.gh[j0]) + (S.gl[i0] - S.gl[j0]);
+                        d = a.reverse ? -d : d;
+                        w[cc][r] = in ? av[cc] * (a.p_scale * ex2_approx(d)) : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+                    *reinterpret_cast<float4 *>(&S.P[4 * tx + cc][4 * ty]) =
+                        make_float4(w[cc][0], w[cc][1], w[cc][2], w[cc][3]);
+                // what the entering state gives
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int d = 0; d < a.dk; ++d) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(&S.Q[d][4 * ty]);
+                    const float4 s4 = *reinterpret_cast<const float4 *>(&S.S[d][4 * tx]);
+                    fma4(acc[0], q4.x, s4);
+                    fma4(acc[1], q4.y, s4);
+                    fma4(acc[2], q4.z, s4);
+                    fma4(acc[3], q4.w, s4);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float f = S.rowf[4 * ty + r];
+                    // a factor of zero is a reset: the state before it does not count
+                    acc[r] = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                      : make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f,
+                                                    acc[r].w * f);
+                }
+            }
+            // the state leaving
+            const float dec = S.decay;
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+                st[r] = dec == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                   : make_float4(st[r].x * dec, st[r].y * dec, st[r].z * dec,
+                                                 st[r].w * dec);
+#pragma unroll 2
+            for (int j = 0; j < kC; j += 4) {
+                const float4 w4 = *reinterpret_cast<const float4 *>(&S.colw[j]);
+                float4 v4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v4[e] = *reinterpret_cast<const float4 *>(&S.V[j + e][4 * tx]);
+                    const float w = e == 0 ? w4.x : e == 1 ? w4.y : e == 2 ? w4.z : w4.w;
+                    v4[e] = make_float4(v4[e].x * w, v4[e].y * w, v4[e].z * w, v4[e].w * w);
+                }
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(&S.K[ty + 16 * r][j]);
+                    fma4(st[r], k4.x, v4[0]);
+                    fma4(st[r], k4.y, v4[1]);
+                    fma4(st[r], k4.z, v4[2]);
+                    fma4(st[r], k4.w, v4[3]);
+                }
+            }
+            if (!kFull && t == 0)
+                seg_log2 += (double)S.decay_log2_h + (double)S.decay_log2_l;
+        }
+        if (!kFull) continue;
+        __syncthreads();  // P is whole
+        if (nq > 0) {
+#pragma unroll 4
+            for (int j = 0; j < kC; ++j) {
+                const float4 p4 = *reinterpret_cast<const float4 *>(&S.P[j][4 * ty]);
+                const float4 v4 = *reinterpret_cast<const float4 *>(&S.V[j][4 * tx]);
+                fma4(acc[0], p4.x, v4);
+                fma4(acc[1], p4.y, v4);
+                fma4(acc[2], p4.z, v4);
+                fma4(acc[3], p4.w, v4);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i0 = 4 * ty + r;
+            const long long tok = row0 + t0 + i0;
+            const float *av = reinterpret_cast<const float *>(&acc[r]);
+            if (a.dot) {  // every lane takes part in the shuffles
+                float d = 0.f;
+                if (i0 < nq) {
+                    const T *dr = static_cast<const T *>(a.dot) + tok * a.dot_row +
+                                  (long long)(h / a.dot_group) * a.dv;
+                    const float4 o = ld4<T>(dr, v0 + 4 * tx, a.dv, vec);
+                    d = fmaf(av[0], o.x, fmaf(av[1], o.y, fmaf(av[2], o.z, av[3] * o.w)));
+                }
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+                if (tx == 0 && i0 < nq)
+                    a.dot_out[((long long)tile * p.batch * p.heads + bh) * p.seqlen + t0 + i0] = d;
+            }
+            if (i0 < nl) {
+                // rows behind the sequence's length are zero
+                const long long off = (tok * p.heads + h) * a.dv + v0 + 4 * tx;
+                if (vec && i0 < nq && v0 + 4 * tx + 4 <= a.dv) {
+                    if (a.y_f32)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.y) + off) = acc[r];
+                    else
+                        st4(static_cast<T *>(a.y) + off, acc[r]);
+                    continue;
+                }
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    if (v0 + 4 * tx + cc >= a.dv) break;
+                    const float o = i0 < nq ? av[cc] : 0.f;
+                    if (a.y_f32)
+                        static_cast<float *>(a.y)[off + cc] = o;
+                    else
+                        static_cast<T *>(a.y)[off + cc] = from_f32<T>(o);
+                }
+            }
+        }
+    }
+
+    float *out = nullptr;
+    bool transposed = false;
+    if (!kFull) {
+        out = a.seg_state + (bh * p.nseg + seg) * state_elems;
+        if (t == 0 && tile == 0) a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
+    } else if (a.h_final && order == p.nseg - 1) {
+        out = a.h_final + bh * state_elems;
+        transposed = a.h_final_t != 0;
+    }
+    if (out) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int d = ty + 16 * r;
+            const float *e = reinterpret_cast<const float *>(&st[r]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int v = v0 + 4 * tx + c;
+                if (d < a.dk && v < a.dv)
+                    out[transposed ? (long long)v * a.dk + d : (long long)d * a.dv + v] = e[c];
+            }
+        }
+    }
+}
+
+// seg_state[s]: the segment's own state -> the state entering it, in the
+// sweep's order. One thread per state element.
+__global__ void __launch_bounds__(kThr) linattn_carry_kernel(const LinattnParams p,
+                                                             long long blocks_per) {
+    const long long id = blockIdx.x / blocks_per;
+    const SweepArgs &a = p.sweep[id % p.nsweeps];
+    const long long bh = id / p.nsweeps;
+    const long long n = (long long)a.dk * a.dv;
+    const long long e = (blockIdx.x % blocks_per) * kThr + threadIdx.x;
+    if (e >= n) return;
+    float h = 0.f;
+    if (a.h_init)
+        h = a.h_init[bh * n + (a.h_init_t ? (e % a.dv) * a.dk + e / a.dv : e)];
+    for (int o = 0; o < p.nseg; ++o) {
+        const int s = a.reverse ? p.nseg - 1 - o : o;
+        float *x = a.seg_state + (bh * p.nseg + s) * n + e;
+        if (o + 1 < p.nseg) {
+            const float own = *x;
+            *x = h;
+            const float dec = __ldg(a.seg_decay + bh * p.nseg + s);
+            h = dec == 0.f ? own : fmaf(dec, h, own);
+        } else {
+            *x = h;
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr)
+linattn_group_sum_kernel(const float *__restrict__ src, T *__restrict__ dst, long long n, int group,
+                         int dim) {
+    for (long long e = (long long)blockIdx.x * kThr + threadIdx.x; e < n;
+         e += (long long)gridDim.x * kThr) {
+        const float *s = src + (e / dim) * group * dim + e % dim;
+        float sum = 0.f;
+        for (int k = 0; k < group; ++k) sum += s[(long long)k * dim];
+        dst[e] = from_f32<T>(sum);
+    }
+}
+
+// dlog_decay_t = X + Σ_{i ≥ t} (q_i·dq_i − k_i·dk_i), X = <S_last, dS_last>:
+// with λ_t the loss's gradient with respect to S_t, <S_t, λ_t> equals both
+// dg_t + k_t·dk_t and q_t·dq_t + dg_{t+1}. The running sum is kept in double:
+// its terms cancel over the sequence, so dg carries the float32 errors of the
+// dot products it sums. Where exp(g_t)·S_{t−1} is zero (a reset; the first
+// token without a first state) dg is zero. One block per (batch row, head), tokens
+// from the last to the first in tiles of 4·1024.
+constexpr int kDgThr = 1024, kDgPer = 4;
+template <typename T>
+__global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const LinattnDecayGrad p) {
+    __shared__ double wsum[32];
+    __shared__ double carry_s;
+    const long long bh = blockIdx.x, b = bh / p.heads;
+    const int h = (int)(bh % p.heads), t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const long long len = p.seqlens
+                              ? min((long long)max(__ldg(p.seqlens + b), 0), p.seqlen)
+                              : p.seqlen;
+    double x = 0.0;
+    if (p.dfinal)
+        for (long long e = t; e < p.state_size; e += kDgThr)
+            x += (double)p.last_state[bh * p.state_size + e] * p.dfinal[bh * p.state_size + e];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    if (lane == 0) wsum[w] = x;
+    __syncthreads();
+    if (t == 0) {
+        double s = 0.0;
+        for (int k = 0; k < 32; ++k) s += wsum[k];
+        carry_s = s;
+    }
+    __syncthreads();
+    double carry = carry_s;
+    const T *g = static_cast<const T *>(p.g) + b * p.seqlen * p.heads + h;
+    T *out = static_cast<T *>(p.dg) + b * p.seqlen * p.heads + h;
+    for (long long i = len + t; i < p.seqlen; i += kDgThr) out[i * p.heads] = from_f32<T>(0.f);
+    const long long plane = p.batch * p.heads * p.seqlen;
+    const float *rows = p.rows + bh * p.seqlen, *cols = p.cols + bh * p.seqlen;
+    for (long long end = len; end > 0; end -= kDgThr * kDgPer) {
+        // thread t takes tokens end − 1 − 4·t − e
+        double v[kDgPer];
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < kDgPer; ++e) {
+            const long long i = end - 1 - (long long)kDgPer * t - e;
+            double d = 0.0;
+            if (i >= 0)
+                for (int k = 0; k < p.tiles; ++k)
+                    d += (double)rows[k * plane + i] - (double)cols[k * plane + i];
+            s += d;
+            v[e] = s;
+        }
+        double incl = s;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, incl, m);
+            if (lane >= m) incl += o;
+        }
+        __syncthreads();  // wsum's readers of the previous tile are done
+        if (lane == 31) wsum[w] = incl;
+        __syncthreads();
+        double before = 0.0, total = 0.0;
+        for (int k = 0; k < 32; ++k) {
+            if (k == w) before = total;
+            total += wsum[k];
+        }
+        const double base = carry + before + (incl - s);
+#pragma unroll
+        for (int e = 0; e < kDgPer; ++e) {
+            const long long i = end - 1 - (long long)kDgPer * t - e;
+            if (i < 0) continue;
+            const bool none = (i == 0 && !p.has_init) ||
+                              (double)ldg_f32(g + i * p.heads) * 1.4426950408889634 < kLaResetLog2;
+            out[i * p.heads] = from_f32<T>(none ? 0.f : (float)(base + v[e]));
+        }
+        carry += total;
+    }
+}
+
+template <typename T, int DKP>
+cudaError_t launch_sweeps(const LinattnParams &p, cudaStream_t stream) {
+    const size_t smem = sizeof(SweepSmem<DKP>);
+    auto full = linattn_sweep_kernel<T, DKP, true>;
+    auto state = linattn_sweep_kernel<T, DKP, false>;
+    cudaError_t e =
+        cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long per_seg = p.batch * p.heads * p.nsweeps * (DKP / kVt);
+    if (p.nseg > 1) {
+        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem, stream>>>(p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    full<<<(unsigned)(per_seg * p.nseg), kThr, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots) {
+    LinattnPlan pl;
+    pl.nchunks = (int)((seqlen + kLaChunk - 1) / kLaChunk);
+    pl.nseg = 1;
+    pl.seg_chunks = pl.nchunks;
+    // estimated time in chunk passes: waves of blocks × chunks a segment; with
+    // several segments the state pass adds about half of it again, and the
+    // carry and the two further launches a few chunks' worth
+    double best = (double)((ctas + slots - 1) / slots) * pl.nchunks;
+    const int most = ctas >= 8ll * slots ? 1 : pl.nchunks < 64 ? pl.nchunks : 64;
+    for (int n = 2; n <= most; ++n) {
+        const int per = (pl.nchunks + n - 1) / n;
+        const int segs = (pl.nchunks + per - 1) / per;
+        const double full = (double)((ctas * segs + slots - 1) / slots) * per;
+        const double own = (double)((ctas * (segs - 1) + slots - 1) / slots) * per * 0.5;
+        const double cost = full + own + 6.0 + 0.05 * segs;
+        if (cost < best) {
+            best = cost;
+            pl.nseg = segs;
+            pl.seg_chunks = per;
+        }
+    }
+    return pl;
+}
+
+int linattn_tiles(int dv) { return dv > kVt ? 2 : 1; }
+
+// Blocks the device holds at a time: two on an SM where both head dimensions
+// fit the 64-wide tiles (85 KB of shared memory each), else one (136 KB).
+int linattn_slots(int dk, int dv) { return dk <= 64 && dv <= 64 ? 2 : 1; }
+
+cudaError_t launch_linattn_sweeps(const LinattnParams &p, bool bf16, cudaStream_t stream) {
+    int most = 0;
+    for (int s = 0; s < p.nsweeps; ++s) most = std::max(most, std::max(p.sweep[s].dk, p.sweep[s].dv));
+    if (bf16)
+        return most <= 64 ? launch_sweeps<__nv_bfloat16, 64>(p, stream)
+                          : launch_sweeps<__nv_bfloat16, 128>(p, stream);
+    return most <= 64 ? launch_sweeps<float, 64>(p, stream) : launch_sweeps<float, 128>(p, stream);
+}
+
+cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream) {
+    const long long n = (long long)p.sweep[0].dk * p.sweep[0].dv;  // the same for every sweep
+    const long long per = (n + kThr - 1) / kThr;
+    linattn_carry_kernel<<<(unsigned)(p.batch * p.heads * p.nsweeps * per), kThr, 0, stream>>>(p, per);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_group_sum(const float *src, void *dst, long long tokens, int qk_heads,
+                                     int group, int dim, bool bf16, cudaStream_t stream) {
+    const long long n = tokens * qk_heads * dim;
+    const unsigned blocks = (unsigned)std::min((n + kThr - 1) / kThr, 1ll << 20);
+    if (bf16)
+        linattn_group_sum_kernel<<<blocks, kThr, 0, stream>>>(
+            src, static_cast<__nv_bfloat16 *>(dst), n, group, dim);
+    else
+        linattn_group_sum_kernel<<<blocks, kThr, 0, stream>>>(src, static_cast<float *>(dst), n,
+                                                              group, dim);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_decay_grad(const LinattnDecayGrad &p, bool bf16, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)(p.batch * p.heads);
+    if (bf16)
+        linattn_decay_grad_kernel<__nv_bfloat16><<<blocks, kDgThr, 0, stream>>>(p);
+    else
+        linattn_decay_grad_kernel<float><<<blocks, kDgThr, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace selscan

@@ -58,6 +58,24 @@ class BwdOptions(ctypes.Structure):
 BBAR_MODES = {"delta": 0, "zoh": 1}
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
+
+
+class LinattnOptions(ctypes.Structure):
+    """selscan_linattn_options_t (include/selscan.h)."""
+    _fields_ = [("log_decay", ctypes.c_void_p), ("head_log_decay", ctypes.c_void_p),
+                ("initial_state", ctypes.c_void_p), ("seqlens", ctypes.c_void_p),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64)]
+
+
+class BlockNormOptions(ctypes.Structure):
+    """selscan_block_norm_options_t (include/selscan.h)."""
+    _fields_ = [("z", ctypes.c_void_p), ("x_stride", _i64), ("z_stride", _i64),
+                ("weight", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("res_scale", ctypes.c_void_p), ("next_weight", ctypes.c_void_p),
+                ("groups", _i64), ("gate", ctypes.c_int), ("residual_f32", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
 
 # name -> (restype, argtypes), mirroring include/selscan.h
 SIGNATURES = {
@@ -95,6 +113,18 @@ SIGNATURES = {
     "selscan_ssd_fwd": (_int, [_vp] * 8 + [_int, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
                                           _int, _vp, _i64, _vp]),
     "selscan_ssd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64]),
+    "selscan_linattn_fwd": (_int, [_vp, _vp, _vp, _f32, ctypes.POINTER(LinattnOptions), _vp, _vp]
+                            + [_i64] * 6 + [_int, _vp, _i64, _vp]),
+    "selscan_linattn_workspace_bytes": (_i64, [_i64] * 6 + [_int]),
+    "selscan_linattn_bwd": (_int, [_vp, _vp, _vp, _f32, ctypes.POINTER(LinattnOptions)]
+                            + [_vp] * 7 + [_i64] * 6 + [_int, _vp, _i64, _vp]),
+    "selscan_linattn_bwd_workspace_bytes": (_i64, [_i64] * 6 + [_int]),
+    "selscan_linattn_step": (_int, [_vp] * 6 + [_f32, _vp] + [_i64] * 5 + [_int, _vp]),
+    "selscan_block_norm_fwd": (_int, [_vp, ctypes.POINTER(BlockNormOptions), _vp, _vp, _i64, _i64,
+                                      _int, _vp]),
+    "selscan_block_norm_bwd": (_int, [_vp, ctypes.POINTER(BlockNormOptions)] + [_vp] * 8
+                               + [_i64, _i64, _int, _vp, _i64, _vp]),
+    "selscan_block_norm_bwd_workspace_bytes": (_i64, [_i64, _i64]),
     "selscan_device_status": (_int, [ctypes.POINTER(_int), _int]),
     "selscan_status_string": (ctypes.c_char_p, [_int]),
     "selscan_last_cuda_error": (ctypes.c_char_p, []),

@@ -48,10 +48,12 @@ int check_dims(const LaDims &d, int dtype) {
     return SELSCAN_OK;
 }
 
-LinattnPlan plan_for(const LaDims &d, int nsweeps) {
-    const int dmax = (int)std::max(d.dk, d.dv);
-    const int64_t ctas = d.pairs() * nsweeps * linattn_tiles(dmax);
-    return linattn_plan(d.seqlen, ctas, sm_count() * linattn_slots((int)d.dk, (int)d.dv));
+// tc: the tensor-core kernels.
+LinattnPlan plan_for(const LaDims &d, int nsweeps, bool tc) {
+    const int64_t ctas = d.pairs() * nsweeps;
+    if (tc) return linattn_plan(d.seqlen, ctas, sm_count(), 3.0, 0.6);
+    return linattn_plan(d.seqlen, ctas * linattn_tiles((int)std::max(d.dk, d.dv)),
+                        sm_count() * linattn_slots((int)d.dk, (int)d.dv), 0.5, 0.5);
 }
 
 // Workspace of one call (offsets in bytes).
@@ -93,7 +95,11 @@ LaLayout layout_for(const LaDims &d, const LinattnPlan &pl, bool bwd) {
 
 int64_t workspace_for(const LaDims &d, int dtype, bool bwd) {
     if (check_dims(d, dtype) != SELSCAN_OK || d.pairs() * d.seqlen == 0) return 0;
-    return (int64_t)layout_for(d, plan_for(d, bwd ? 3 : 1), bwd).total;
+    // the larger of the two paths' (which one runs depends on the operands' rows)
+    const int n = bwd ? 3 : 1;
+    size_t total = layout_for(d, plan_for(d, n, false), bwd).total;
+    if (d.bf16) total = std::max(total, layout_for(d, plan_for(d, n, true), bwd).total);
+    return (int64_t)total;
 }
 
 // Checks shared by the forward and the gradient, on the operands and options.
@@ -233,7 +239,11 @@ int selscan_linattn_fwd(const void *q, const void *k, const void *v, float scale
         const cudaError_t e = set_state(final_state, h0, d.state_bytes(), stream);
         return e == cudaSuccess ? SELSCAN_OK : cuda_fail(e);
     }
-    const LinattnPlan pl = plan_for(d, 1);
+    const bool tc = d.bf16 && linattn_tc_rows(q, in.q_row, (int)dk, seqlen) &&
+                    linattn_tc_rows(k, in.k_row, (int)dk, seqlen) &&
+                    linattn_tc_rows(v, in.v_row, (int)dv, seqlen) &&
+                    linattn_tc_rows(y, heads * dv, (int)dv, seqlen);
+    const LinattnPlan pl = plan_for(d, 1, tc);
     const LaLayout l = layout_for(d, pl, false);
     void *ws = nullptr;
     rc = take_workspace(&ws, workspace, workspace_bytes, l.total, outs, 2, ins, ni, stream);
@@ -258,7 +268,10 @@ int selscan_linattn_fwd(const void *q, const void *k, const void *v, float scale
         a.seg_state = reinterpret_cast<float *>(w + l.seg_state[0]);
         a.seg_decay = reinterpret_cast<float *>(w + l.seg_decay[0]);
     }
-    return finish(launch_linattn_sweeps(p, d.bf16, stream), ws, !workspace, stream);
+    cudaError_t e = device_status_address(&p.status);
+    if (e == cudaSuccess)
+        e = tc ? launch_linattn_tc(p, stream) : launch_linattn_sweeps(p, d.bf16, stream);
+    return finish(e, ws, !workspace, stream);
 }
 
 int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale,
@@ -299,7 +312,16 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
         const cudaError_t e = set_state(dinitial_state, dfinal_state, d.state_bytes(), stream);
         return e == cudaSuccess ? SELSCAN_OK : cuda_fail(e);
     }
-    const LinattnPlan pl = plan_for(d, 3);
+    const bool shared = heads != qk_heads;
+    const bool tc = d.bf16 && linattn_tc_rows(q, in.q_row, (int)dk, seqlen) &&
+                    linattn_tc_rows(k, in.k_row, (int)dk, seqlen) &&
+                    linattn_tc_rows(v, in.v_row, (int)dv, seqlen) &&
+                    linattn_tc_rows(dy, heads * dv, (int)dv, seqlen) &&
+                    (shared || (linattn_tc_rows(dq, heads * dk, (int)dk, seqlen) &&
+                                linattn_tc_rows(dk_, heads * dk, (int)dk, seqlen))) &&
+                    linattn_tc_rows(dv_, heads * dv, (int)dv, seqlen) &&
+                    seqlen * heads * std::max(dk, dv) < (1ll << 37);
+    const LinattnPlan pl = plan_for(d, 3, tc);
     const LaLayout l = layout_for(d, pl, true);
     void *ws = nullptr;
     rc = take_workspace(&ws, workspace, workspace_bytes, l.total, outs, 5, ins, ni, stream);
@@ -307,7 +329,6 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
     char *w = static_cast<char *>(ws);
     LinattnParams p = base_params(d, in, pl);
     p.nsweeps = 3;
-    const bool shared = heads != qk_heads;
     p.vec = rows_vec(q, in.q_row, dk, d.es) && rows_vec(k, in.k_row, dk, d.es) &&
             rows_vec(v, in.v_row, dv, d.es) && rows_vec(dy, heads * dv, dv, d.es) &&
             (shared || (!misaligned(dq, 4 * d.es) && !misaligned(dk_, 4 * d.es))) &&
@@ -370,7 +391,9 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
         a.h_init = dfinal_state;
         a.h_final = dinitial_state;
     }
-    cudaError_t e = launch_linattn_sweeps(p, d.bf16, stream);
+    cudaError_t e = device_status_address(&p.status);
+    if (e == cudaSuccess)
+        e = tc ? launch_linattn_tc(p, stream) : launch_linattn_sweeps(p, d.bf16, stream);
     if (shared) {
         const float *src[2] = {reinterpret_cast<float *>(w + l.dq),
                                reinterpret_cast<float *>(w + l.dk)};
@@ -383,7 +406,7 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
         LinattnDecayGrad g{};
         g.rows = reinterpret_cast<const float *>(w + l.rows);
         g.cols = reinterpret_cast<const float *>(w + l.cols);
-        g.tiles = linattn_tiles((int)dk);
+        g.tiles = tc ? 1 : linattn_tiles((int)dk);  // the tensor-core blocks hold all columns
         g.dfinal = dfinal_state;
         g.last_state = reinterpret_cast<const float *>(w + l.last_state);
         g.state_size = dk * dv;

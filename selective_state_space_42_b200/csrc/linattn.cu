@@ -546,22 +546,24 @@ cudaError_t launch_sweeps(const LinattnParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots) {
+LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots, double head, double own) {
     LinattnPlan pl;
     pl.nchunks = (int)((seqlen + kLaChunk - 1) / kLaChunk);
     pl.nseg = 1;
     pl.seg_chunks = pl.nchunks;
-    // estimated time in chunk passes: waves of blocks × chunks a segment; with
-    // several segments the state pass adds about half of it again, and the
-    // carry and the two further launches a few chunks' worth
-    double best = (double)((ctas + slots - 1) / slots) * pl.nchunks;
+    // estimated time in chunk passes: waves of blocks × (start-up + chunks a
+    // segment); with several segments also the state pass, the carry and the
+    // two further launches
+    double best = (double)((ctas + slots - 1) / slots) * (head + pl.nchunks);
     const int most = ctas >= 8ll * slots ? 1 : pl.nchunks < 64 ? pl.nchunks : 64;
     for (int n = 2; n <= most; ++n) {
         const int per = (pl.nchunks + n - 1) / n;
         const int segs = (pl.nchunks + per - 1) / per;
-        const double full = (double)((ctas * segs + slots - 1) / slots) * per;
-        const double own = (double)((ctas * (segs - 1) + slots - 1) / slots) * per * 0.5;
-        const double cost = full + own + 6.0 + 0.05 * segs;
+        if (segs < 2) continue;
+        const double cost =
+            (double)((ctas * segs + slots - 1) / slots) * (head + per) +
+            (double)((ctas * (segs - 1) + slots - 1) / slots) * (head + own * per) + 6.0 +
+            0.05 * segs;
         if (cost < best) {
             best = cost;
             pl.nseg = segs;

@@ -37,7 +37,7 @@ struct SweepArgs {
     int h_init_t, h_final_t;
     float *seg_state;             // [batch·heads][nseg][dk][dv]: segments' states
     float *seg_decay;             // [batch·heads][nseg]
-    int map[4];                   // tensor-core path: tensor maps of q, k, v, dot
+    int map[4], map_y;            // tensor-core path: tensor maps of q, k, v, dot and y
 };
 
 struct LinattnParams {
@@ -63,7 +63,9 @@ constexpr double kLaResetLog2 = -160.0;
 struct LinattnPlan {
     int nchunks, nseg, seg_chunks;
 };
-LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots);
+// `head`: a block's start-up, `own`: the state pass's time, in chunk passes
+// and as a share of the full pass.
+LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots, double head, double own);
 
 // CUDA-core path: any sizes and alignment, both I/O types.
 int linattn_tiles(int dv);  // 64-column tiles of a sweep (blocks per head and segment)
@@ -71,6 +73,11 @@ int linattn_slots(int dk, int dv);
 cudaError_t launch_linattn_sweeps(const LinattnParams &p, bool bf16, cudaStream_t stream);
 // Carry: seg_state[s] becomes the state entering segment s.
 cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream);
+
+// Tensor-core path (linattn_tc.cu): bfloat16 I/O, operands whose rows TMA can
+// read (16-byte rows and bases, dims multiples of 8); one block an SM.
+bool linattn_tc_rows(const void *ptr, long long row, int dim, long long seqlen);
+cudaError_t launch_linattn_tc(const LinattnParams &p, cudaStream_t stream);
 
 // Sum of the `group` heads that share one query/key head:
 // src [tokens][qk_heads][group][dim] float32 -> dst [tokens][qk_heads][dim].

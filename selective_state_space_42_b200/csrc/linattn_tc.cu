@@ -1,0 +1,773 @@
+// linattn_tc.cu -- linear attention with a decay for each head on the
+// fifth-generation tensor cores: the sweep of linattn_params.cuh for bfloat16
+// I/O, one persistent pass over the tokens with the state kept on the chip.
+//
+// Per (batch row, head), chunks of 64 tokens (formulas in linattn.cu). The
+// state S is held transposed, value column d on tensor-memory lane d:
+//   scores   A = Q Kᵀ                       64 (of 128) × 64 × D
+//   Yi       (P V)ᵀ = Vᵀ Pᵀ, P = A ◦ weights     128 × 64 × 64
+//   Ye       (Q S_in)ᵀ = S_inᵀ Qᵀ           128 × 64 × D
+//   U        Σ_j c_j·v_j k_jᵀ = (c ◦ V)ᵀ K  128 × D × 64
+//   y = Yi + r_i·Ye,   S ← exp(G_end)·S + U
+// Q, K, V (and in the gradient the operand of the dot product) come by TMA into
+// a ring of stages, 128-byte swizzled; P is written to shared memory; S_in and
+// c ◦ V are A operands in tensor memory. Warps (20, one block an SM):
+//   0-1    P: scores from tensor memory, weights exp(G_i − G_j), to bfloat16
+//   2      TMA producer, and each chunk's prefix sums of the log decays
+//   3      issues every MMA (one thread)
+//   4-7    c ◦ V: lane d reads column d of V, scales and splits it
+//   8-15   state: half of a row's D columns per warp group, float32 registers
+//   16-19  outputs: y to shared memory, TMA store; the gradient's dot products
+// Precision: P and (in the forward pass) S_in are rounded once to bfloat16, an
+// error of the output's own rounding on each of many terms; c ◦ V is split
+// into three bfloat16 parts, so that the state, a float32 result that is
+// carried over the whole sequence, keeps 24 bits. The gradient needs its
+// products with S_in to about 16 bits instead (its log decays' gradient sums
+// q·dq − k·dk, which cancel), so there S_in is a high/low pair and c ◦ V two
+// parts (17 bits): both fill the 512 columns of tensor memory.
+#include "linattn_params.cuh"
+#include "umma_util.cuh"
+
+#include <algorithm>
+
+namespace selscan {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+
+constexpr int kC = kLaChunk;
+constexpr uint64_t kWaitNs = 2000000000ull;  // every wait gives up after 2 s
+constexpr int kStatusLinattnWait = 6;         // device error code
+constexpr int kThr = 640;
+constexpr int kWarpTma = 2, kWarpMma = 3;
+constexpr int kMaps = 8;
+
+struct TcMaps {
+    CUtensorMap m[kMaps];
+};
+
+// ---- tensor memory -------------------------------------------------------------
+// 16 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
+// The same of two column ranges at once.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16],
+                                            float (&b)[16]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "[%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(ta), "r"(tb)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        a[k] = __uint_as_float(r[k]);
+        b[k] = __uint_as_float(r[16 + k]);
+    }
+}
+// 8 columns of this thread's lane (completed by tmem_st_wait).
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                   "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D (tensor memory) = A (tensor memory, lane = row, two K elements a column) · B (shared memory).
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// ---- TMA -------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int c0,
+                                             int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+        ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2),
+          "r"(c3)
+        : "memory");
+}
+
+// Byte offset of (token j, column d) in a tile of 64-column slabs of 64 rows,
+// 128-byte swizzled.
+__device__ __forceinline__ uint32_t tile_off(int j, int d) {
+    return (uint32_t)((d >> 6) * (kC * 128) + j * 128 + ((((d >> 3) & 7) ^ (j & 7)) << 4) +
+                      (d & 7) * 2);
+}
+
+// ---- sizes -------------------------------------------------------------------------
+// Tensor-memory columns.
+template <int D, bool kBwd> struct Cols {
+    static constexpr uint32_t S = 0, Yi = 64, Ye = 128, U = 192;
+    static constexpr uint32_t St = U + D, StParts = kBwd ? 2 : 1;
+    static constexpr uint32_t Vp = St + StParts * (D / 2), VpParts = kBwd ? 2 : 3;
+    static_assert(Vp + VpParts * 32 <= 512, "tensor memory");
+};
+
+template <int D, bool kBwd> struct TcSmem {
+    static constexpr int kTiles = kBwd ? 4 : 3;  // q, k, v (, dot)
+    static constexpr int kStages = kBwd ? 2 : 3;
+    bf16 tile[kStages][kTiles][kC * D];
+    bf16 P[kC * kC];
+    float out[kC * D];              // y on its way out: bfloat16 or float32 rows in slabs
+    float G[kStages][kC];           // prefix sums of the log decays times log2 e
+    float rowf[kStages][kC], colw[kStages][kC];
+    float decay[kStages];
+    float red[4][kC];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t s_full, s_empty, p_full, p_empty, vp_full, u_full, u_empty, st_full, st_empty;
+    uint64_t o_full, o_empty, drain;
+    uint64_t v_sync, o_sync;        // the four c ◦ V warps, the four output warps
+    uint32_t tmem;
+    int abort;
+};
+
+// One value per token for this lane (v[i], i = 0 .. 31) -> the sum over the
+// warp's lanes of v[lane] in lane `lane`: halves are exchanged and added.
+__device__ __forceinline__ float lanes_sum32(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int k = 0; k < m; ++k) {
+            const float send = up ? v[k] : v[k + m];
+            const float keep = up ? v[k + m] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    }
+    return v[0];
+}
+
+// One block: one (sweep, batch row, head, segment). kFull false: only the
+// segment's own state, from zero.
+template <int D, bool kBwd, bool kFull>
+__global__ void __launch_bounds__(kThr, 1)
+linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant__ TcMaps maps) {
+    typedef TcSmem<D, kBwd> Smem;
+    typedef Cols<D, kBwd> C;
+    constexpr int kStages = Smem::kStages;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
+    Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                        ~static_cast<uintptr_t>(1023));
+    const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
+    const int order = (int)(blockIdx.x % nruns);    // position in the sweep's direction
+    const long long id = blockIdx.x / nruns;
+    const SweepArgs &a = p.sweep[id % p.nsweeps];
+    const long long bh = id / p.nsweeps;
+    const int b = (int)(bh / p.heads), h = (int)(bh % p.heads);
+    const bool rev = a.reverse != 0;
+    const int seg = rev ? p.nseg - 1 - order : order;
+    const int len = p.seqlens ? (int)min((long long)max(__ldg(p.seqlens + b), 0), p.seqlen)
+                              : (int)p.seqlen;
+    const int c_first = seg * p.seg_chunks, c_end = min(p.nchunks, c_first + p.seg_chunks);
+    const int c_live = max(c_first, min(c_end, (len + kC - 1) / kC));  // chunks with tokens
+    const int n = c_live - c_first;
+    auto chunk_of = [&](int i) { return rev ? c_live - 1 - i : c_first + i; };
+    const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
+    const bool has_dot = kBwd && kFull && a.dot_out != nullptr;
+
+    if (warp == kWarpTma) tmem_alloc(&S.tmem, 512);
+    if (t == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&S.full[s], 2);
+            mbar_init(&S.empty[s], kFull ? 19 : 13);
+        }
+        mbar_init(&S.s_full, 1);
+        mbar_init(&S.s_empty, 2);
+        mbar_init(&S.p_full, 2);
+        mbar_init(&S.p_empty, 1);
+        mbar_init(&S.vp_full, 4);
+        mbar_init(&S.u_full, 1);
+        mbar_init(&S.u_empty, 8);
+        mbar_init(&S.st_full, 8);
+        mbar_init(&S.st_empty, 1);
+        mbar_init(&S.o_full, 1);
+        mbar_init(&S.o_empty, 4);
+        mbar_init(&S.drain, 1);
+        mbar_init(&S.v_sync, 4);
+        mbar_init(&S.o_sync, 4);
+        S.abort = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // this warp's lanes
+    // A wait of a whole warp; false once any role has given up.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, &S.abort, kWaitNs));
+    };
+    auto arrive = [&](uint64_t *bar) {  // by one lane for the warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    bool ok = true;
+
+    if (warp == kWarpTma) {
+        // ---- producer: tiles by TMA, decays by the warp -----------------------------
+        const CUtensorMap *mq = &maps.m[a.map[0]], *mk = &maps.m[a.map[1]],
+                          *mv = &maps.m[a.map[2]], *md = &maps.m[a.map[3]];
+        const int hq = h / a.q_group, hk = h / a.k_group, hv = h / a.v_group,
+                  hd = has_dot ? h / a.dot_group : 0;
+        const float gh = p.g ? 0.f : p.g_head ? __ldg(p.g_head + h) : 0.f;
+        auto raw = [&](int i, int e) -> float {  // the log decay of token 2·lane + e of chunk i
+            const int tok = chunk_of(i) * kC + 2 * lane + e;
+            if (i >= n || tok >= len) return 0.f;
+            return p.g ? ldg_f32(static_cast<const bf16 *>(p.g) +
+                                 ((long long)b * p.seqlen + tok) * p.heads + h)
+                       : gh;
+        };
+        float r0 = raw(0, 0), r1 = raw(0, 1);
+        double seg_log2 = 0.0;
+        int issued = 0;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages;
+            ok = wait(&S.empty[s], ((i / kStages) & 1) ^ 1);
+            if (!ok) break;
+            const int t0 = chunk_of(i) * kC;
+            if (lane == 0) {
+                constexpr int kSlabs = D / 64;
+                constexpr uint32_t kBytes = kSlabs * kC * 128;
+                mbar_arrive_expect_tx(&S.full[s],
+                                      kBytes * (kFull ? (has_dot ? 4 : 3) : 2));
+#pragma unroll
+                for (int sl = 0; sl < kSlabs; ++sl) {
+                    if (kFull)
+                        tma_load_4d(&S.tile[s][0][sl * kC * 64], mq, &S.full[s], sl * 64, hq, t0, b);
+                    tma_load_4d(&S.tile[s][1][sl * kC * 64], mk, &S.full[s], sl * 64, hk, t0, b);
+                    tma_load_4d(&S.tile[s][2][sl * kC * 64], mv, &S.full[s], sl * 64, hv, t0, b);
+                    if (has_dot)
+                        tma_load_4d(&S.tile[s][Smem::kTiles - 1][sl * kC * 64], md, &S.full[s],
+                                    sl * 64, hd, t0, b);
+                }
+            }
+            issued = i + 1;
+            double g0 = (double)r0 * 1.4426950408889634, g1 = (double)r1 * 1.4426950408889634;
+            r0 = raw(i + 1, 0);
+            r1 = raw(i + 1, 1);
+            g0 = g0 < kLaResetLog2 ? kLaResetLog2 : g0;
+            g1 = g1 < kLaResetLog2 ? kLaResetLog2 : g1;
+            double sum = g0 + g1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(0xffffffffu, sum, m);
+                if (lane >= m) sum += o;
+            }
+            const double end = __shfl_sync(0xffffffffu, sum, 31);
+            const double G[2] = {sum - g1, sum};
+            float up[2], down[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                up[e] = ex2_approx((float)G[e]);
+                down[e] = ex2_approx((float)(end - G[e]));
+            }
+            *reinterpret_cast<float2 *>(&S.G[s][2 * lane]) = make_float2((float)G[0], (float)G[1]);
+            *reinterpret_cast<float2 *>(&S.rowf[s][2 * lane]) =
+                make_float2(a.row_scale * (rev ? down[0] : up[0]),
+                            a.row_scale * (rev ? down[1] : up[1]));
+            *reinterpret_cast<float2 *>(&S.colw[s][2 * lane]) =
+                make_float2(a.col_scale * (rev ? up[0] : down[0]),
+                            a.col_scale * (rev ? up[1] : down[1]));
+            if (lane == 0) S.decay[s] = ex2_approx((float)end);
+            seg_log2 += end;
+            arrive(&S.full[s]);
+        }
+        if (!kFull && lane == 0)
+            a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
+        if (!ok) {  // copies still in flight land before the block goes
+            const int none = 0;
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(&S.full[i % kStages], (i / kStages) & 1, &none, kWaitNs);
+        }
+    } else if (warp == kWarpMma) {
+        // ---- MMA issuer ---------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
+            constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
+            constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
+            constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
+            constexpr uint32_t kSlab = kC * 128;
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity & 1, &S.abort, kWaitNs);
+                tc_fence_after();
+                return ok;
+            };
+            auto kmajor = [&](uint32_t base, int k) {  // K step k of 16 columns
+                return umma_desc_sw128(base + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024);
+            };
+            auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
+                const int s = i % kStages;
+                if (!wait1(&S.full[s], i / kStages) || !wait1(&S.s_empty, (i & 1) ^ 1)) return;
+                const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_bf16(tmem + C::S, kmajor(q, x), kmajor(k, x), id_s, x > 0);
+                umma_commit(&S.s_full);
+            };
+            if (kFull && n > 0) scores(0);
+            for (int i = 0; ok && i < n; ++i) {
+                const int s = i % kStages;
+                const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]),
+                               v = smem_addr(S.tile[s][2]);
+                // U: both operands' K is the token (16 tokens = two 8-row atoms of a slab)
+                if (!wait1(&S.full[s], i / kStages) || !wait1(&S.vp_full, i & 1) ||
+                    !wait1(&S.u_empty, (i & 1) ^ 1))
+                    break;
+#pragma unroll
+                for (int part = 0; part < (int)C::VpParts; ++part)
+#pragma unroll
+                    for (int x = 0; x < kC / 16; ++x)
+                        umma_bf16_ts(tmem + C::U, tmem + C::Vp + part * 32 + x * 8,
+                                     umma_desc_sw128(k + x * 2048, kSlab, 1024), id_u,
+                                     part > 0 || x > 0);
+                umma_commit(&S.u_full);
+                if (!kFull) {
+                    umma_commit(&S.empty[s]);
+                    continue;
+                }
+                if (i + 1 < n) scores(i + 1);
+                // Ye and Yi
+                if (!ok || !wait1(&S.o_empty, (i & 1) ^ 1) || !wait1(&S.st_full, i & 1)) break;
+#pragma unroll
+                for (int part = 0; part < (int)C::StParts; ++part)
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+                        umma_bf16_ts(tmem + C::Ye, tmem + C::St + part * (D / 2) + x * 8,
+                                     kmajor(q, x), id_ye, part > 0 || x > 0);
+                umma_commit(&S.st_empty);
+                if (!wait1(&S.p_full, i & 1)) break;
+                const uint32_t pp = smem_addr(S.P);
+#pragma unroll
+                for (int x = 0; x < kC / 16; ++x)
+                    umma_bf16(tmem + C::Yi, umma_desc_sw128(v + x * 2048, kSlab, 1024),
+                              umma_desc_sw128(pp + x * 32, 16, 1024), id_yi, x > 0);
+                umma_commit(&S.o_full);
+                umma_commit(&S.p_empty);
+                umma_commit(&S.empty[s]);
+            }
+            if (!ok) {  // MMAs in flight end before tensor memory is given back
+                const int none = 0;
+                umma_commit(&S.drain);
+                mbar_wait(&S.drain, 0, &none, kWaitNs);
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    } else if (warp < 2) {
+        // ---- P: weights of the products inside the chunk ------------------------------
+        if (kFull) {
+            const int r = 32 * warp + lane;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % kStages;
+                const int nq = min(kC, len - chunk_of(i) * kC);
+                ok = wait(&S.full[s], i / kStages) && wait(&S.s_full, i & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float gr = S.G[s][r];
+                uint4 out[8];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    // 16 columns; all masked for the warp: no scores are read
+                    if (rev ? 16 * q4 + 15 < 32 * warp : 16 * q4 > 32 * warp + 31) {
+                        out[2 * q4] = out[2 * q4 + 1] = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    float v[16];
+                    tmem_ld16(tmem + lanes + C::S + 16 * q4, v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = 16 * q4 + e;
+                        const bool in = (rev ? j >= r : j <= r) && r < nq && j < nq;
+                        const float d = rev ? S.G[s][j] - gr : gr - S.G[s][j];
+                        v[e] = in ? v[e] * (a.p_scale * ex2_approx(d)) : 0.f;
+                    }
+                    out[2 * q4] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    out[2 * q4 + 1] =
+                        make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]),
+                                   pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
+                }
+                tc_fence_before();
+                arrive(&S.s_empty);
+                arrive(&S.empty[s]);
+                ok = wait(&S.p_empty, (i & 1) ^ 1);
+                if (!ok) break;
+                char *row = reinterpret_cast<char *>(S.P) + r * 128;
+#pragma unroll
+                for (int c8 = 0; c8 < 8; ++c8)
+                    *reinterpret_cast<uint4 *>(row + ((c8 ^ (r & 7)) << 4)) = out[c8];
+                fence_proxy_async_smem();
+                arrive(&S.p_full);
+            }
+        }
+    } else if (warp < 8) {
+        // ---- c ◦ V as bfloat16 parts, column d of V on lane d --------------------------
+        const int d = 32 * (warp & 3) + lane;
+        uint32_t syncs = 0;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages;
+            const int nq = min(kC, len - chunk_of(i) * kC);
+            ok = wait(&S.full[s], i / kStages);
+            if (!ok) break;
+            if (nq < kC && len < p.seqlen) {
+                // what stands behind the row's length may be anything: zero it
+                for (int e = t - 128; e < (kC - nq) * (D / 8); e += 128) {
+                    const uint32_t off = tile_off(nq + e / (D / 8), 8 * (e % (D / 8)));
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][1]) + off) =
+                        make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][2]) + off) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                arrive(&S.v_sync);
+                ok = wait(&S.v_sync, syncs++);
+                if (!ok) break;
+            }
+            if (i > 0) {
+                ok = wait(&S.u_full, (i - 1) & 1);  // U has read the previous parts
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (d < D) {
+                const char *tile = reinterpret_cast<const char *>(S.tile[s][2]);
+#pragma unroll
+                for (int j16 = 0; j16 < kC / 16; ++j16) {
+                    uint32_t part[3][8];
+#pragma unroll
+                    for (int e2 = 0; e2 < 8; ++e2) {
+                        const int j = 16 * j16 + 2 * e2;
+                        const float2 w = *reinterpret_cast<const float2 *>(&S.colw[s][j]);
+                        float x0 = w.x * __bfloat162float(*reinterpret_cast<const bf16 *>(
+                                             tile + tile_off(j, d)));
+                        float x1 = w.y * __bfloat162float(*reinterpret_cast<const bf16 *>(
+                                             tile + tile_off(j + 1, d)));
+#pragma unroll
+                        for (int k = 0; k < (int)C::VpParts; ++k) {
+                            const uint32_t u = pack_bf16x2(x0, x1);
+                            part[k][e2] = u;
+                            x0 -= __uint_as_float(u << 16);
+                            x1 -= __uint_as_float(u & 0xFFFF0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < (int)C::VpParts; ++k)
+                        tmem_st8(tmem + lanes + C::Vp + k * 32 + 8 * j16, part[k]);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            arrive(&S.vp_full);
+            arrive(&S.empty[s]);
+        }
+    } else if (warp < 16) {
+        // ---- state: lane d, columns half·D/2 .. ------------------------------------------
+        constexpr int kH = D / 2;
+        const int d = 32 * (warp & 3) + lane, half = (warp - 8) >> 2;
+        const long long elems = (long long)a.dk * a.dv;
+        float st[kH];
+        {
+            const float *src = nullptr;
+            bool tr = false;
+            if (kFull && p.nseg > 1) {
+                src = a.seg_state + (bh * p.nseg + seg) * elems;
+            } else if (kFull && a.h_init) {
+                src = a.h_init + bh * elems;
+                tr = a.h_init_t != 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kH; ++k) {
+                const int c = half * kH + k;
+                st[k] = src && d < a.dv && c < a.dk
+                            ? src[tr ? (long long)d * a.dk + c : (long long)c * a.dv + d] : 0.f;
+            }
+        }
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages;
+            if (kFull) {
+                ok = wait(&S.st_empty, (i & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (d < D) {
+#pragma unroll
+                    for (int k16 = 0; k16 < kH / 16; ++k16) {
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x0 = st[16 * k16 + 2 * e], x1 = st[16 * k16 + 2 * e + 1];
+                            hi[e] = pack_bf16x2(x0, x1);
+                            lo[e] = pack_bf16x2(x0 - __uint_as_float(hi[e] << 16),
+                                                x1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+                        }
+                        const uint32_t at = tmem + lanes + C::St + half * (kH / 2) + 8 * k16;
+                        tmem_st8(at, hi);
+                        if (kBwd) tmem_st8(at + D / 2, lo);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                arrive(&S.st_full);
+            }
+            ok = wait(&S.full[s], i / kStages) && wait(&S.u_full, i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const float dec = S.decay[s];
+            if (d < D) {
+#pragma unroll
+                for (int k16 = 0; k16 < kH / 16; ++k16) {
+                    float u[16];
+                    tmem_ld16(tmem + lanes + C::U + half * kH + 16 * k16, u);
+                    // a decay of zero resets: the old state does not count
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        st[16 * k16 + e] = dec == 0.f ? u[e] : fmaf(dec, st[16 * k16 + e], u[e]);
+                }
+            }
+            tc_fence_before();
+            arrive(&S.u_empty);
+            arrive(&S.empty[s]);
+        }
+        float *dst = nullptr;
+        bool tr = false;
+        if (!kFull) {
+            dst = a.seg_state + (bh * p.nseg + seg) * elems;
+        } else if (a.h_final && order == p.nseg - 1) {
+            dst = a.h_final + bh * elems;
+            tr = a.h_final_t != 0;
+        }
+        if (dst && d < a.dv) {
+#pragma unroll
+            for (int k = 0; k < kH; ++k) {
+                const int c = half * kH + k;
+                if (c < a.dk) dst[tr ? (long long)d * a.dk + c : (long long)c * a.dv + d] = st[k];
+            }
+        }
+    } else if (kFull) {
+        // ---- outputs: lane d, a column per token -----------------------------------------
+        const int d = 32 * (warp & 3) + lane;
+        const int tl = t - 512;  // 0 .. 127
+        const CUtensorMap *my = &maps.m[a.map_y];
+        const bool f32 = kBwd && a.y_f32;
+        uint32_t syncs = 0;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages;
+            const int t0 = chunk_of(i) * kC, nq = min(kC, len - t0);
+            ok = wait(&S.full[s], i / kStages) && wait(&S.o_full, i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (tl == 0) bulk_wait_read<0>();  // the previous chunk's store has read the staging
+            arrive(&S.o_sync);
+            ok = wait(&S.o_sync, syncs++);
+            if (!ok) break;
+            if (d < D) {
+#pragma unroll
+                for (int j32 = 0; j32 < 2; ++j32) {
+                    float dv[32];
+#pragma unroll
+                    for (int j16 = 0; j16 < 2; ++j16) {
+                        const int j0 = 32 * j32 + 16 * j16;
+                        float yi[16], ye[16];
+                        tmem_ld16x2(tmem + lanes + C::Yi + j0, tmem + lanes + C::Ye + j0, yi, ye);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int j = j0 + e;
+                            const float f = S.rowf[s][j];
+                            // a factor of zero is a reset; rows behind the length are zero
+                            float y = f == 0.f ? yi[e] : fmaf(f, ye[e], yi[e]);
+                            y = j < nq ? y : 0.f;
+                            if (f32)
+                                S.out[(d >> 5) * (kC * 32) + j * 32 + (d & 31)] = y;
+                            else
+                                reinterpret_cast<bf16 *>(S.out)[(d >> 6) * (kC * 64) + j * 64 +
+                                                                (d & 63)] = __float2bfloat16_rn(y);
+                            if (kBwd && has_dot) {
+                                const bf16 o = *reinterpret_cast<const bf16 *>(
+                                    reinterpret_cast<const char *>(S.tile[s][Smem::kTiles - 1]) +
+                                    tile_off(j, d));
+                                dv[16 * j16 + e] = j < nq ? y * __bfloat162float(o) : 0.f;
+                            }
+                        }
+                    }
+                    if (kBwd && has_dot) S.red[warp & 3][32 * j32 + lane] = lanes_sum32(dv);
+                }
+            }
+            tc_fence_before();
+            arrive(&S.o_empty);
+            arrive(&S.empty[s]);
+            fence_proxy_async_smem();
+            arrive(&S.o_sync);
+            ok = wait(&S.o_sync, syncs++);
+            if (!ok) break;
+            if (tl == 0) {
+                if (f32) {
+                    for (int c = 0; c < a.dv; c += 32)
+                        tma_store_4d(my, S.out + (c >> 5) * (kC * 32), c, h, t0, b);
+                } else {
+                    for (int c = 0; c < a.dv; c += 64)
+                        tma_store_4d(my, reinterpret_cast<bf16 *>(S.out) + (c >> 6) * (kC * 64), c,
+                                     h, t0, b);
+                }
+                bulk_commit();
+            }
+            if (kBwd && has_dot && tl < nq) {
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) sum += S.red[w][tl];
+                a.dot_out[bh * p.seqlen + t0 + tl] = sum;
+            }
+        }
+        if (tl == 0) bulk_wait<0>();  // the last stores are out before the block ends
+        // chunks without a token: zeros
+        const long long row0 = (long long)b * p.seqlen;
+        for (long long tok = (long long)c_live * kC; tok < min((long long)c_end * kC, p.seqlen);
+             ++tok) {
+            const long long off = ((row0 + tok) * p.heads + h) * a.dv + tl;
+            if (tl >= a.dv) continue;
+            if (f32)
+                static_cast<float *>(a.y)[off] = 0.f;
+            else
+                static_cast<bf16 *>(a.y)[off] = __float2bfloat16_rn(0.f);
+        }
+    }
+
+    if (!ok && lane == 0) {  // the others stop waiting too
+        *reinterpret_cast<volatile int *>(&S.abort) = 1;
+        if (p.status) atomicCAS(p.status, 0, kStatusLinattnWait);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpTma) tmem_dealloc(tmem, 512);
+}
+
+// ---- host ---------------------------------------------------------------------------
+// [batch][seqlen][heads][dim] with `row` elements between tokens: boxes of 64
+// tokens and 128 bytes.
+bool make_map(CUtensorMap *m, const void *base, long long batch, long long seqlen, int heads,
+              int dim, long long row, bool f32, bool swizzle) {
+    auto fn = tma_encode();
+    if (!fn) return false;
+    const cuuint64_t es = f32 ? 4 : 2;
+    cuuint64_t gdim[4] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)seqlen, (cuuint64_t)batch};
+    cuuint64_t gstride[3] = {(cuuint64_t)dim * es, (cuuint64_t)row * es,
+                             (cuuint64_t)(seqlen * row) * es};
+    cuuint32_t box[4] = {f32 ? 32u : 64u, 1, (cuuint32_t)kC, 1};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void *>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kBwd>
+cudaError_t launch(const LinattnParams &p, const TcMaps &maps, cudaStream_t stream) {
+    const int smem = (int)sizeof(TcSmem<D, kBwd>) + 1024;
+    auto full = linattn_tc_kernel<D, kBwd, true>;
+    auto state = linattn_tc_kernel<D, kBwd, false>;
+    cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long per_seg = p.batch * p.heads * p.nsweeps;
+    if (p.nseg > 1) {
+        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem, stream>>>(p, maps);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    full<<<(unsigned)(per_seg * p.nseg), kThr, smem, stream>>>(p, maps);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool linattn_tc_rows(const void *ptr, long long row, int dim, long long seqlen) {
+    return dim % 8 == 0 && row % 8 == 0 && (reinterpret_cast<uintptr_t>(ptr) & 15) == 0 &&
+           seqlen < (1ll << 30) && seqlen * row < (1ll << 38);
+}
+
+cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) {
+    LinattnParams p = params;
+    TcMaps maps{};
+    int n = 0;
+    // one map per distinct operand
+    struct Key {
+        const void *ptr;
+        long long row;
+        int dim, heads;
+    } keys[kMaps];
+    auto operand = [&](const void *ptr, long long row, int dim, int group) -> int {
+        const int heads = p.heads / group;
+        for (int i = 0; i < n; ++i)
+            if (keys[i].ptr == ptr && keys[i].row == row && keys[i].dim == dim &&
+                keys[i].heads == heads)
+                return i;
+        if (n >= kMaps || !make_map(&maps.m[n], ptr, p.batch, p.seqlen, heads, dim, row, false, true))
+            return -1;
+        keys[n] = Key{ptr, row, dim, heads};
+        return n++;
+    };
+    int most = 0;
+    for (int s = 0; s < p.nsweeps; ++s) {
+        SweepArgs &a = p.sweep[s];
+        a.map[0] = operand(a.q, a.q_row, a.dk, a.q_group);
+        a.map[1] = operand(a.k, a.k_row, a.dk, a.k_group);
+        a.map[2] = operand(a.v, a.v_row, a.dv, a.v_group);
+        a.map[3] = a.dot ? operand(a.dot, a.dot_row, a.dv, a.dot_group) : 0;
+        if (a.map[0] < 0 || a.map[1] < 0 || a.map[2] < 0 || a.map[3] < 0) return cudaErrorInvalidValue;
+        most = std::max(most, std::max(a.dk, a.dv));
+    }
+    for (int s = 0; s < p.nsweeps; ++s) {
+        SweepArgs &a = p.sweep[s];
+        if (n >= kMaps || !make_map(&maps.m[n], a.y, p.batch, p.seqlen, p.heads, a.dv,
+                                    (long long)p.heads * a.dv, a.y_f32 != 0, false))
+            return cudaErrorInvalidValue;
+        keys[n] = Key{nullptr, 0, 0, 0};
+        a.map_y = n++;
+    }
+    if (p.nsweeps == 1)
+        return most <= 64 ? launch<64, false>(p, maps, stream) : launch<128, false>(p, maps, stream);
+    return most <= 64 ? launch<64, true>(p, maps, stream) : launch<128, true>(p, maps, stream);
+}
+
+}  // namespace selscan

@@ -33,11 +33,8 @@
 // of 16 bytes along the tile's contiguous dimension). Accumulators are
 // float32 in tensor memory; one elected thread issues every MMA and a
 // tcgen05.commit to an mbarrier tells the CTA they are done.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "ssd_params.cuh"
-#include "tma_util.cuh"
+#include "umma_util.cuh"
 
 #include <algorithm>
 #include <cstddef>
@@ -62,25 +59,6 @@ __device__ __forceinline__ uint32_t core_off(int r, int c) {
     return (uint32_t)(((r >> 3) * (kCols >> 3) + (c >> 3)) * 128 + (r & 7) * 16 + (c & 7) * 2);
 }
 
-// Shared-memory matrix descriptor, no swizzle: start address, leading byte
-// offset (stride between core matrices along K), stride byte offset (along
-// M or N), descriptor version 1.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
-}
-
-// The same for the 128-byte swizzled layout (layout type 2): 8-row atoms of
-// 128-byte rows whose 16-byte chunks are permuted by the row index, as a
-// 128B-swizzled TMA load writes them. K-major: the start advances by 32
-// bytes per K step of 16 inside a 64-column slab; the stride byte offset is
-// the distance between 8-row atoms (1024 bytes). M/N-major: leading byte
-// offset = distance between 64-element slabs, stride byte offset = between
-// 8-row atoms along K.
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return umma_desc(saddr, lbo, sbo) | (2ull << 61);
-}
-
 // 3-D tiled TMA load (coordinates innermost first) completing on an mbarrier.
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int32_t c0, int32_t c1, int32_t c2) {
@@ -99,77 +77,6 @@ __device__ __forceinline__ void tma_bc_tile(bf16 *tile, const CUtensorMap *map, 
                                             int t0, int b) {
     tma_load_3d(tile, map, bar, 0, t0, b);
     tma_load_3d(tile + kQ * 64, map, bar, 64, t0, b);
-}
-
-// Instruction descriptor of kind::f16: bfloat16 A and B, float32 D, shape
-// M×N, each operand K-major (0) or M/N-major (1).
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-        ::"r"(smem_addr(bar))
-        : "memory");
-}
-
-// Whole-warp tensor-memory allocation of ncols columns (a power of two ≥ 32);
-// the base address lands in *dst.
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(smem_addr(dst)), "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// 32 consecutive float32 columns of this thread's lane (shape 32x32b: the
-// warp reads its own 32 lanes).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Eight floats as bfloat16 pairs v = hi + lo: hi is v with its low 16 bits
@@ -886,21 +793,6 @@ ssd_tc_out_kernel(const SsdParams p, const __grid_constant__ CUtensorMap tm_b,
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 256);
-}
-
-// cuTensorMapEncodeTiled from the driver (through the runtime's entry-point
-// query, so the library links against the runtime only).
-PFN_cuTensorMapEncodeTiled_v12000 tma_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void *ptr = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
 }
 
 // A [batch][seqlen][dstate] bfloat16 tensor (B or C) as a 3-D map with

@@ -36,11 +36,18 @@ namespace {
 typedef __nv_bfloat16 bf16;
 
 constexpr int kC = kLaChunk;
-constexpr uint64_t kWaitNs = 2000000000ull;  // every wait gives up after 2 s
+constexpr long long kWaitClocks = 4000000000ll;  // every wait gives up after about 2 s
 constexpr int kStatusLinattnWait = 6;         // device error code
 constexpr int kThr = 640;
+constexpr int kSlots = 8;                     // ring of the chunks' decay factors
 constexpr int kWarpTma = 2, kWarpMma = 3;
 constexpr int kMaps = 8;
+
+template <bool kV> struct Flag {
+    static constexpr bool value = kV;
+};
+typedef Flag<true> Yes;
+typedef Flag<false> No;
 
 struct TcMaps {
     CUtensorMap m[kMaps];
@@ -109,6 +116,34 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// Waits for the phase of `bar` with the given parity; false once *abort is set
+// or the time is up. Timed by the SM's clock: a wait stands between two MMAs
+// here, and reading the global timer at its start was measured to delay the
+// waiting thread by about a microsecond.
+__device__ __forceinline__ bool try_wait_hint(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)  // may sleep up to 20 us
+        : "memory");
+    return ok != 0;
+}
+// Out of line: the roles' loops share the instruction caches.
+__device__ __noinline__ bool wait_bar_slow(uint64_t *bar, uint32_t parity, const int *abort) {
+    const long long start = clock64();
+    for (;;) {
+        if (try_wait_hint(bar, parity)) return true;
+        if (*reinterpret_cast<const volatile int *>(abort)) return false;
+        if (clock64() - start > kWaitClocks) return false;
+    }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int *abort) {
+    return mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity, abort);
+}
+
 // ---- TMA -------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int c0, int c1, int c2, int c3) {
@@ -146,28 +181,29 @@ template <int D, bool kBwd> struct Cols {
 
 template <int D, bool kBwd> struct TcSmem {
     static constexpr int kTiles = kBwd ? 4 : 3;  // q, k, v (, dot)
-    static constexpr int kStages = kBwd ? 2 : 3;
+    static constexpr int kStages = 3;
     bf16 tile[kStages][kTiles][kC * D];
     bf16 P[kC * kC];
-    float out[kC * D];              // y on its way out: bfloat16 or float32 rows in slabs
-    float G[kStages][kC];           // prefix sums of the log decays times log2 e
-    float rowf[kStages][kC], colw[kStages][kC];
-    float decay[kStages];
+    bf16 out[kC * D];               // y on its way out: slabs of 64 columns
+    float G[kSlots][kC];            // prefix sums of the log decays times log2 e
+    float rowf[kSlots][kC], colw[kSlots][kC];
+    float decay[kSlots];
+    int reset[kSlots];              // a factor in rowf is zero
     float red[4][kC];
     uint64_t full[kStages], empty[kStages];
     uint64_t s_full, s_empty, p_full, p_empty, vp_full, u_full, u_empty, st_full, st_empty;
     uint64_t o_full, o_empty, drain;
-    uint64_t v_sync, o_sync;        // the four c ◦ V warps, the four output warps
+    uint64_t v_sync, o_sync;        // the c ◦ V warps, the output warps
     uint32_t tmem;
     int abort;
 };
 
-// One value per token for this lane (v[i], i = 0 .. 31) -> the sum over the
-// warp's lanes of v[lane] in lane `lane`: halves are exchanged and added.
-__device__ __forceinline__ float lanes_sum32(float (&v)[32]) {
+// One value per token for this lane (v[i], i = 0 .. 15) -> the sum over the
+// warp's lanes of v[lane mod 16] in lane `lane`: halves are exchanged and added.
+__device__ __forceinline__ float lanes_sum16(float (&v)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
+    for (int m = 8; m > 0; m >>= 1) {
         const bool up = (lane & m) != 0;
 #pragma unroll
         for (int k = 0; k < m; ++k) {
@@ -176,7 +212,80 @@ __device__ __forceinline__ float lanes_sum32(float (&v)[32]) {
             v[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+// 32 columns of row r of P as packed bfloat16: scores times p·2^(G_r − G_j)
+// (reverse: p·2^(G_j − G_r)), zero outside columns lo .. hi. gr = G_r + log2 |p|
+// (reverse: G_r − log2 |p|).
+template <bool kRev>
+__device__ __forceinline__ void score_weights(const float (&v)[32], const float *G, float gr,
+                                              int lo, int hi, uint32_t (&out)[16]) {
+#pragma unroll
+    for (int e4 = 0; e4 < 8; ++e4) {
+        const float4 g4 = *reinterpret_cast<const float4 *>(G + 4 * e4);
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // selects, not branches
+            const int j = 4 * e4 + e;
+            const float w = v[j] * ex2_approx(kRev ? g[e] - gr : gr - g[e]);
+            x[e] = j >= lo && j <= hi ? w : 0.f;
+        }
+        out[2 * e4] = pack_bf16x2(x[0], x[1]);
+        out[2 * e4 + 1] = pack_bf16x2(x[2], x[3]);
+    }
+}
+
+// A chunk's outputs y = Yi + r ◦ Ye of value column d (this thread's lane) into
+// the staging rows (kF32: to float32 rows in memory, nl of them), and with kDot
+// the products with the dot operand summed over the warp's columns. kReset: a
+// factor r of zero is a reset, and Ye does not count whatever it is. Rows
+// behind the sequence's length come out zero (their operands are zero). Token
+// pairs are rounded together.
+template <int D, bool kBwd, bool kF32, bool kDot, bool kReset>
+__device__ __forceinline__ void output_rows(TcSmem<D, kBwd> &S, uint32_t tmem, int s,
+                                            const float *rowf, int d, float *y, long long y_row,
+                                            int nl) {
+    typedef Cols<D, kBwd> C;
+    char *out = reinterpret_cast<char *>(S.out) + (d >> 6) * (kC * 128) + (d & 63) * 2;
+    const char *dot = reinterpret_cast<const char *>(S.tile[s][TcSmem<D, kBwd>::kTiles - 1]);
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kC; j0 += 16) {
+        float yi[16], ye[16];
+        tmem_ld16x2(tmem + C::Yi + j0, tmem + C::Ye + j0, yi, ye);
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(rowf + j0 + 4 * e4);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 4 * e4 + e;
+                yi[k] = kReset && f[e] == 0.f ? yi[k] : fmaf(f[e], ye[k], yi[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            if (kF32) {
+                if (y && j0 + k < nl) y[(j0 + k) * y_row] = yi[k];
+                if (y && j0 + k + 1 < nl) y[(j0 + k + 1) * y_row] = yi[k + 1];
+            } else {
+                const uint32_t u = pack_bf16x2(yi[k], yi[k + 1]);
+                *reinterpret_cast<uint16_t *>(out + (j0 + k) * 128) = (uint16_t)u;
+                *reinterpret_cast<uint16_t *>(out + (j0 + k) * 128 + 128) = (uint16_t)(u >> 16);
+            }
+        }
+        if (kDot) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                yi[k] *= __bfloat162float(
+                    *reinterpret_cast<const bf16 *>(dot + j0 * 128 + tile_off(k, d)));
+            const float sum = lanes_sum16(yi);
+            if (lane < 16) S.red[(threadIdx.x >> 5) & 3][j0 + lane] = sum;
+        }
+    }
 }
 
 // One block: one (sweep, batch row, head, segment). kFull false: only the
@@ -189,8 +298,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     constexpr int kStages = Smem::kStages;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
-    Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                        ~static_cast<uintptr_t>(1023));
+    Smem &S = *reinterpret_cast<Smem *>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
     const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
     const int order = (int)(blockIdx.x % nruns);    // position in the sweep's direction
     const long long id = blockIdx.x / nruns;
@@ -212,7 +320,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     if (t == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&S.full[s], 2);
-            mbar_init(&S.empty[s], kFull ? 19 : 13);
+            mbar_init(&S.empty[s], has_dot ? 5 : 1);  // the MMAs (and the dot operand's readers)
         }
         mbar_init(&S.s_full, 1);
         mbar_init(&S.s_empty, 2);
@@ -238,14 +346,17 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // this warp's lanes
     // A wait of a whole warp; false once any role has given up.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, &S.abort, kWaitNs));
+        return __all_sync(0xffffffffu, wait_bar(bar, parity & 1, &S.abort));
     };
     auto arrive = [&](uint64_t *bar) {  // by one lane for the warp
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
     bool ok = true;
-
+    // Chunk i's factors stand in slot i % kSlots. The producer runs at most
+    // kStages chunks ahead of the MMAs, every reader of chunk i is done before
+    // the MMAs of chunk i + 2, so eight slots need no barrier of their own.
+    if (warp < 4) {
     if (warp == kWarpTma) {
         // ---- producer: tiles by TMA, decays by the warp -----------------------------
         const CUtensorMap *mq = &maps.m[a.map[0]], *mk = &maps.m[a.map[1]],
@@ -304,14 +415,18 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 up[e] = ex2_approx((float)G[e]);
                 down[e] = ex2_approx((float)(end - G[e]));
             }
-            *reinterpret_cast<float2 *>(&S.G[s][2 * lane]) = make_float2((float)G[0], (float)G[1]);
-            *reinterpret_cast<float2 *>(&S.rowf[s][2 * lane]) =
+            const int sl = i % kSlots;
+            *reinterpret_cast<float2 *>(&S.G[sl][2 * lane]) = make_float2((float)G[0], (float)G[1]);
+            *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) =
                 make_float2(a.row_scale * (rev ? down[0] : up[0]),
                             a.row_scale * (rev ? down[1] : up[1]));
-            *reinterpret_cast<float2 *>(&S.colw[s][2 * lane]) =
+            *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) =
                 make_float2(a.col_scale * (rev ? up[0] : down[0]),
                             a.col_scale * (rev ? up[1] : down[1]));
-            if (lane == 0) S.decay[s] = ex2_approx((float)end);
+            if (lane == 0) S.decay[sl] = ex2_approx((float)end);
+            const bool none = (rev ? down[0] : up[0]) == 0.f || (rev ? down[1] : up[1]) == 0.f;
+            const bool reset = __any_sync(0xffffffffu, none);
+            if (lane == 0) S.reset[sl] = reset;
             seg_log2 += end;
             arrive(&S.full[s]);
         }
@@ -320,42 +435,47 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         if (!ok) {  // copies still in flight land before the block goes
             const int none = 0;
             for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(&S.full[i % kStages], (i / kStages) & 1, &none, kWaitNs);
+                wait_bar(&S.full[i % kStages], (i / kStages) & 1, &none);
         }
     } else if (warp == kWarpMma) {
         // ---- MMA issuer ---------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
-            constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
-            constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
-            constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
-            constexpr uint32_t kSlab = kC * 128;
-            auto wait1 = [&](uint64_t *bar, uint32_t parity) {
-                ok = ok && mbar_wait(bar, parity & 1, &S.abort, kWaitNs);
-                tc_fence_after();
-                return ok;
-            };
-            auto kmajor = [&](uint32_t base, int k) {  // K step k of 16 columns
-                return umma_desc_sw128(base + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024);
-            };
-            auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
-                const int s = i % kStages;
-                if (!wait1(&S.full[s], i / kStages) || !wait1(&S.s_empty, (i & 1) ^ 1)) return;
-                const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]);
+        // The warp waits (a lane per barrier, so that two waits cost one), lane 0 issues.
+        constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
+        constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
+        constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
+        constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
+        constexpr uint32_t kSlab = kC * 128;
+        auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) -> bool {
+            bool done = true;
+            if (lane < 2) done = wait_bar(lane ? b1 : b0, (lane ? p1 : p0) & 1, &S.abort);
+            ok = __all_sync(0xffffffffu, done);
+            tc_fence_after();
+            return ok;
+        };
+        auto kmajor = [&](uint32_t base, int k) {  // K step k of 16 columns
+            return umma_desc_sw128(base + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024);
+        };
+        auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
+            const int s = i % kStages;
+            if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
+            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]);
+            if (lane == 0) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
                     umma_bf16(tmem + C::S, kmajor(q, x), kmajor(k, x), id_s, x > 0);
                 umma_commit(&S.s_full);
-            };
-            if (kFull && n > 0) scores(0);
-            for (int i = 0; ok && i < n; ++i) {
-                const int s = i % kStages;
-                const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]),
-                               v = smem_addr(S.tile[s][2]);
-                // U: both operands' K is the token (16 tokens = two 8-row atoms of a slab)
-                if (!wait1(&S.full[s], i / kStages) || !wait1(&S.vp_full, i & 1) ||
-                    !wait1(&S.u_empty, (i & 1) ^ 1))
-                    break;
+            }
+            __syncwarp();
+        };
+        if (kFull && n > 0) scores(0);
+        for (int i = 0; ok && i < n; ++i) {
+            const int s = i % kStages;
+            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]),
+                           v = smem_addr(S.tile[s][2]);
+            // U: both operands' K is the token (16 tokens = two 8-row atoms of a slab). Its
+            // tiles have landed: c ◦ V was made from them.
+            if (!wait2(&S.vp_full, i, &S.u_empty, (i & 1) ^ 1)) break;
+            if (lane == 0) {
 #pragma unroll
                 for (int part = 0; part < (int)C::VpParts; ++part)
 #pragma unroll
@@ -364,13 +484,14 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                                      umma_desc_sw128(k + x * 2048, kSlab, 1024), id_u,
                                      part > 0 || x > 0);
                 umma_commit(&S.u_full);
-                if (!kFull) {
-                    umma_commit(&S.empty[s]);
-                    continue;
-                }
-                if (i + 1 < n) scores(i + 1);
-                // Ye and Yi
-                if (!ok || !wait1(&S.o_empty, (i & 1) ^ 1) || !wait1(&S.st_full, i & 1)) break;
+                if (!kFull) umma_commit(&S.empty[s]);
+            }
+            __syncwarp();
+            if (!kFull) continue;
+            if (i + 1 < n) scores(i + 1);
+            // Ye and Yi
+            if (!ok || !wait2(&S.o_empty, (i & 1) ^ 1, &S.st_full, i)) break;
+            if (lane == 0) {
 #pragma unroll
                 for (int part = 0; part < (int)C::StParts; ++part)
 #pragma unroll
@@ -378,7 +499,10 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                         umma_bf16_ts(tmem + C::Ye, tmem + C::St + part * (D / 2) + x * 8,
                                      kmajor(q, x), id_ye, part > 0 || x > 0);
                 umma_commit(&S.st_empty);
-                if (!wait1(&S.p_full, i & 1)) break;
+            }
+            __syncwarp();
+            if (!wait2(&S.p_full, i, &S.p_full, i)) break;
+            if (lane == 0) {
                 const uint32_t pp = smem_addr(S.P);
 #pragma unroll
                 for (int x = 0; x < kC / 16; ++x)
@@ -388,60 +512,68 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 umma_commit(&S.p_empty);
                 umma_commit(&S.empty[s]);
             }
-            if (!ok) {  // MMAs in flight end before tensor memory is given back
-                const int none = 0;
-                umma_commit(&S.drain);
-                mbar_wait(&S.drain, 0, &none, kWaitNs);
-            }
+            __syncwarp();
         }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-    } else if (warp < 2) {
+        if (!ok) {  // MMAs in flight end before tensor memory is given back
+            const int none = 0;
+            if (lane == 0) {
+                umma_commit(&S.drain);
+                wait_bar(&S.drain, 0, &none);
+            }
+            __syncwarp();
+        }
+    } else {
         // ---- P: weights of the products inside the chunk ------------------------------
         if (kFull) {
             const int r = 32 * warp + lane;
+            // the products' scale goes into the exponent, its sign onto the result
+            const float log_p = lg2_approx(fabsf(a.p_scale));
+            const uint32_t sign_p = a.p_scale < 0.f ? 0x80008000u : 0u;
             for (int i = 0; i < n; ++i) {
                 const int s = i % kStages;
                 const int nq = min(kC, len - chunk_of(i) * kC);
                 ok = wait(&S.full[s], i / kStages) && wait(&S.s_full, i & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const float gr = S.G[s][r];
-                uint4 out[8];
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    // 16 columns; all masked for the warp: no scores are read
-                    if (rev ? 16 * q4 + 15 < 32 * warp : 16 * q4 > 32 * warp + 31) {
-                        out[2 * q4] = out[2 * q4 + 1] = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    float v[16];
-                    tmem_ld16(tmem + lanes + C::S + 16 * q4, v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int j = 16 * q4 + e;
-                        const bool in = (rev ? j >= r : j <= r) && r < nq && j < nq;
-                        const float d = rev ? S.G[s][j] - gr : gr - S.G[s][j];
-                        v[e] = in ? v[e] * (a.p_scale * ex2_approx(d)) : 0.f;
-                    }
-                    out[2 * q4] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                    out[2 * q4 + 1] =
-                        make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]),
-                                   pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
-                }
-                tc_fence_before();
-                arrive(&S.s_empty);
-                arrive(&S.empty[s]);
-                ok = wait(&S.p_empty, (i & 1) ^ 1);
-                if (!ok) break;
+                const float *G = S.G[i % kSlots];
+                const float gr = G[r] + (rev ? -log_p : log_p);
+                const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
                 char *row = reinterpret_cast<char *>(S.P) + r * 128;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t out[16];
+                    if (rev ? half < warp : half > warp) {  // all masked for the warp
 #pragma unroll
-                for (int c8 = 0; c8 < 8; ++c8)
-                    *reinterpret_cast<uint4 *>(row + ((c8 ^ (r & 7)) << 4)) = out[c8];
+                        for (int k = 0; k < 16; ++k) out[k] = 0;
+                    } else {
+                        float v[32];
+                        tmem_ld32(tmem + lanes + C::S + 32 * half, v);
+                        if (rev)
+                            score_weights<true>(v, G + 32 * half, gr, lo - 32 * half,
+                                                hi - 32 * half, out);
+                        else
+                            score_weights<false>(v, G + 32 * half, gr, lo - 32 * half,
+                                                 hi - 32 * half, out);
+                    }
+                    if (half == 0)
+                        ok = wait(&S.p_empty, (i & 1) ^ 1);
+                    else {
+                        tc_fence_before();
+                        arrive(&S.s_empty);  // the next chunk's scores may come
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int c8 = 0; c8 < 4; ++c8)
+                        *reinterpret_cast<uint4 *>(row + (((4 * half + c8) ^ (r & 7)) << 4)) =
+                            make_uint4(out[4 * c8] ^ sign_p, out[4 * c8 + 1] ^ sign_p,
+                                       out[4 * c8 + 2] ^ sign_p, out[4 * c8 + 3] ^ sign_p);
+                }
+                if (!ok) break;
                 fence_proxy_async_smem();
                 arrive(&S.p_full);
             }
         }
+    }
     } else if (warp < 8) {
         // ---- c ◦ V as bfloat16 parts, column d of V on lane d --------------------------
         const int d = 32 * (warp & 3) + lane;
@@ -455,10 +587,10 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 // what stands behind the row's length may be anything: zero it
                 for (int e = t - 128; e < (kC - nq) * (D / 8); e += 128) {
                     const uint32_t off = tile_off(nq + e / (D / 8), 8 * (e % (D / 8)));
-                    *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][1]) + off) =
-                        make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][2]) + off) =
-                        make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                    for (int x = kFull ? 0 : 1; x < Smem::kTiles; ++x)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][x]) + off) =
+                            make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 arrive(&S.v_sync);
@@ -472,20 +604,26 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             }
             if (d < D) {
                 const char *tile = reinterpret_cast<const char *>(S.tile[s][2]);
-#pragma unroll
+                // rolled: the loop bodies of the five roles share the instruction caches
+#pragma unroll 1
                 for (int j16 = 0; j16 < kC / 16; ++j16) {
                     uint32_t part[3][8];
 #pragma unroll
                     for (int e2 = 0; e2 < 8; ++e2) {
-                        const int j = 16 * j16 + 2 * e2;
-                        const float2 w = *reinterpret_cast<const float2 *>(&S.colw[s][j]);
+                        const int j = 2 * e2;  // of the 16 tokens (the swizzle's period is 8)
+                        const float2 w =
+                            *reinterpret_cast<const float2 *>(&S.colw[i % kSlots][16 * j16 + j]);
                         float x0 = w.x * __bfloat162float(*reinterpret_cast<const bf16 *>(
-                                             tile + tile_off(j, d)));
+                                             tile + 2048 * j16 + tile_off(j, d)));
                         float x1 = w.y * __bfloat162float(*reinterpret_cast<const bf16 *>(
-                                             tile + tile_off(j + 1, d)));
+                                             tile + 2048 * j16 + tile_off(j + 1, d)));
 #pragma unroll
                         for (int k = 0; k < (int)C::VpParts; ++k) {
-                            const uint32_t u = pack_bf16x2(x0, x1);
+                            // all parts but the last by truncation (no conversion)
+                            const uint32_t u =
+                                k + 1 < (int)C::VpParts
+                                    ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
+                                    : pack_bf16x2(x0, x1);
                             part[k][e2] = u;
                             x0 -= __uint_as_float(u << 16);
                             x1 -= __uint_as_float(u & 0xFFFF0000u);
@@ -499,7 +637,6 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             }
             tc_fence_before();
             arrive(&S.vp_full);
-            arrive(&S.empty[s]);
         }
     } else if (warp < 16) {
         // ---- state: lane d, columns half·D/2 .. ------------------------------------------
@@ -552,21 +689,24 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             ok = wait(&S.full[s], i / kStages) && wait(&S.u_full, i & 1);
             if (!ok) break;
             tc_fence_after();
-            const float dec = S.decay[s];
+            const float dec = S.decay[i % kSlots];
             if (d < D) {
 #pragma unroll
                 for (int k16 = 0; k16 < kH / 16; ++k16) {
                     float u[16];
                     tmem_ld16(tmem + lanes + C::U + half * kH + 16 * k16, u);
-                    // a decay of zero resets: the old state does not count
+                    if (dec == 0.f) {  // a reset: the old state does not count
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        st[16 * k16 + e] = dec == 0.f ? u[e] : fmaf(dec, st[16 * k16 + e], u[e]);
+                        for (int e = 0; e < 16; ++e) st[16 * k16 + e] = u[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            st[16 * k16 + e] = fmaf(dec, st[16 * k16 + e], u[e]);
+                    }
                 }
             }
             tc_fence_before();
             arrive(&S.u_empty);
-            arrive(&S.empty[s]);
         }
         float *dst = nullptr;
         bool tr = false;
@@ -583,7 +723,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (c < a.dk) dst[tr ? (long long)d * a.dk + c : (long long)c * a.dv + d] = st[k];
             }
         }
-    } else if (kFull) {
+    } else {
+        if (kFull) {
         // ---- outputs: lane d, a column per token -----------------------------------------
         const int d = 32 * (warp & 3) + lane;
         const int tl = t - 512;  // 0 .. 127
@@ -601,53 +742,46 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             ok = wait(&S.o_sync, syncs++);
             if (!ok) break;
             if (d < D) {
-#pragma unroll
-                for (int j32 = 0; j32 < 2; ++j32) {
-                    float dv[32];
-#pragma unroll
-                    for (int j16 = 0; j16 < 2; ++j16) {
-                        const int j0 = 32 * j32 + 16 * j16;
-                        float yi[16], ye[16];
-                        tmem_ld16x2(tmem + lanes + C::Yi + j0, tmem + lanes + C::Ye + j0, yi, ye);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int j = j0 + e;
-                            const float f = S.rowf[s][j];
-                            // a factor of zero is a reset; rows behind the length are zero
-                            float y = f == 0.f ? yi[e] : fmaf(f, ye[e], yi[e]);
-                            y = j < nq ? y : 0.f;
-                            if (f32)
-                                S.out[(d >> 5) * (kC * 32) + j * 32 + (d & 31)] = y;
-                            else
-                                reinterpret_cast<bf16 *>(S.out)[(d >> 6) * (kC * 64) + j * 64 +
-                                                                (d & 63)] = __float2bfloat16_rn(y);
-                            if (kBwd && has_dot) {
-                                const bf16 o = *reinterpret_cast<const bf16 *>(
-                                    reinterpret_cast<const char *>(S.tile[s][Smem::kTiles - 1]) +
-                                    tile_off(j, d));
-                                dv[16 * j16 + e] = j < nq ? y * __bfloat162float(o) : 0.f;
-                            }
-                        }
-                    }
-                    if (kBwd && has_dot) S.red[warp & 3][32 * j32 + lane] = lanes_sum32(dv);
+                // float32 rows (the heads' parts of a shared gradient) go straight to memory
+                const int nl = (int)min((long long)kC, p.seqlen - t0);
+                const long long y_row = (long long)p.heads * a.dv;
+                float *yf = f32 && d < a.dv
+                                ? static_cast<float *>(a.y) +
+                                      ((long long)b * p.seqlen + t0) * y_row + h * a.dv + d
+                                : nullptr;
+                const uint32_t at = tmem + lanes;
+                const float *rowf = S.rowf[i % kSlots];
+                auto rows = [&](auto is_f32, auto is_dot) {
+                    if (S.reset[i % kSlots])
+                        output_rows<D, kBwd, decltype(is_f32)::value, decltype(is_dot)::value, true>(
+                            S, at, s, rowf, d, yf, y_row, nl);
+                    else
+                        output_rows<D, kBwd, decltype(is_f32)::value, decltype(is_dot)::value, false>(
+                            S, at, s, rowf, d, yf, y_row, nl);
+                };
+                if constexpr (kBwd) {
+                    if (has_dot && f32)
+                        rows(Yes(), Yes());
+                    else if (has_dot)
+                        rows(No(), Yes());
+                    else if (f32)
+                        rows(Yes(), No());
+                    else
+                        rows(No(), No());
+                } else {
+                    rows(No(), No());
                 }
             }
             tc_fence_before();
             arrive(&S.o_empty);
-            arrive(&S.empty[s]);
+            if (has_dot) arrive(&S.empty[s]);
             fence_proxy_async_smem();
             arrive(&S.o_sync);
             ok = wait(&S.o_sync, syncs++);
             if (!ok) break;
-            if (tl == 0) {
-                if (f32) {
-                    for (int c = 0; c < a.dv; c += 32)
-                        tma_store_4d(my, S.out + (c >> 5) * (kC * 32), c, h, t0, b);
-                } else {
-                    for (int c = 0; c < a.dv; c += 64)
-                        tma_store_4d(my, reinterpret_cast<bf16 *>(S.out) + (c >> 6) * (kC * 64), c,
-                                     h, t0, b);
-                }
+            if (tl == 0 && !f32) {
+                for (int c = 0; c < a.dv; c += 64)
+                    tma_store_4d(my, S.out + (c >> 6) * (kC * 64), c, h, t0, b);
                 bulk_commit();
             }
             if (kBwd && has_dot && tl < nq) {
@@ -663,11 +797,12 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         for (long long tok = (long long)c_live * kC; tok < min((long long)c_end * kC, p.seqlen);
              ++tok) {
             const long long off = ((row0 + tok) * p.heads + h) * a.dv + tl;
-            if (tl >= a.dv) continue;
+            if (tl >= a.dv) break;
             if (f32)
                 static_cast<float *>(a.y)[off] = 0.f;
             else
                 static_cast<bf16 *>(a.y)[off] = __float2bfloat16_rn(0.f);
+        }
         }
     }
 
@@ -682,19 +817,18 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
 
 // ---- host ---------------------------------------------------------------------------
 // [batch][seqlen][heads][dim] with `row` elements between tokens: boxes of 64
-// tokens and 128 bytes.
+// tokens and 64 columns.
 bool make_map(CUtensorMap *m, const void *base, long long batch, long long seqlen, int heads,
-              int dim, long long row, bool f32, bool swizzle) {
+              int dim, long long row, bool swizzle) {
     auto fn = tma_encode();
     if (!fn) return false;
-    const cuuint64_t es = f32 ? 4 : 2;
     cuuint64_t gdim[4] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)seqlen, (cuuint64_t)batch};
-    cuuint64_t gstride[3] = {(cuuint64_t)dim * es, (cuuint64_t)row * es,
-                             (cuuint64_t)(seqlen * row) * es};
-    cuuint32_t box[4] = {f32 ? 32u : 64u, 1, (cuuint32_t)kC, 1};
+    cuuint64_t gstride[3] = {(cuuint64_t)dim * 2, (cuuint64_t)row * 2,
+                             (cuuint64_t)(seqlen * row) * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)kC, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
-    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-              const_cast<void *>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim, gstride, box,
+              estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -742,7 +876,7 @@ cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) 
             if (keys[i].ptr == ptr && keys[i].row == row && keys[i].dim == dim &&
                 keys[i].heads == heads)
                 return i;
-        if (n >= kMaps || !make_map(&maps.m[n], ptr, p.batch, p.seqlen, heads, dim, row, false, true))
+        if (n >= kMaps || !make_map(&maps.m[n], ptr, p.batch, p.seqlen, heads, dim, row, true))
             return -1;
         keys[n] = Key{ptr, row, dim, heads};
         return n++;
@@ -759,8 +893,9 @@ cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) 
     }
     for (int s = 0; s < p.nsweeps; ++s) {
         SweepArgs &a = p.sweep[s];
+        if (a.y_f32) continue;  // stored without TMA
         if (n >= kMaps || !make_map(&maps.m[n], a.y, p.batch, p.seqlen, p.heads, a.dv,
-                                    (long long)p.heads * a.dv, a.y_f32 != 0, false))
+                                    (long long)p.heads * a.dv, false))
             return cudaErrorInvalidValue;
         keys[n] = Key{nullptr, 0, 0, 0};
         a.map_y = n++;

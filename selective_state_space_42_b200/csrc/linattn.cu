@@ -163,7 +163,7 @@ __device__ __forceinline__ void chunk_decays(const LinattnParams &p, const Sweep
 // One block: one (sweep, batch row, head, segment, 64 value columns).
 // kFull false: only the segment's own state, from zero.
 template <typename T, int DKP, bool kFull>
-__global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const LinattnParams p) {
+__global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_constant__ LinattnParams p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SweepSmem<DKP> &S = *reinterpret_cast<SweepSmem<DKP> *>(smem_raw);
     const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
@@ -407,17 +407,18 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const LinattnParams
 
 // seg_state[s]: the segment's own state -> the state entering it, in the
 // sweep's order. One thread per state element.
-__global__ void __launch_bounds__(kThr) linattn_carry_kernel(const LinattnParams p,
-                                                             long long blocks_per) {
-    const long long id = blockIdx.x / blocks_per;
-    const SweepArgs &a = p.sweep[id % p.nsweeps];
-    const long long bh = id / p.nsweeps;
-    const long long n = (long long)a.dk * a.dv;
-    const long long e = (blockIdx.x % blocks_per) * kThr + threadIdx.x;
+__global__ void __launch_bounds__(kThr)
+linattn_carry_kernel(const __grid_constant__ LinattnParams p, unsigned blocks_per) {
+    const unsigned id = blockIdx.x / blocks_per;
+    const SweepArgs &a = p.sweep[id % (unsigned)p.nsweeps];
+    const long long bh = id / (unsigned)p.nsweeps;
+    const int n = a.dk * a.dv;
+    const int e = (int)(blockIdx.x % blocks_per) * kThr + (int)threadIdx.x;
     if (e >= n) return;
     float h = 0.f;
     if (a.h_init)
         h = a.h_init[bh * n + (a.h_init_t ? (e % a.dv) * a.dk + e / a.dv : e)];
+#pragma unroll 4
     for (int o = 0; o < p.nseg; ++o) {
         const int s = a.reverse ? p.nseg - 1 - o : o;
         float *x = a.seg_state + (bh * p.nseg + s) * n + e;
@@ -591,7 +592,8 @@ cudaError_t launch_linattn_sweeps(const LinattnParams &p, bool bf16, cudaStream_
 cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream) {
     const long long n = (long long)p.sweep[0].dk * p.sweep[0].dv;  // the same for every sweep
     const long long per = (n + kThr - 1) / kThr;
-    linattn_carry_kernel<<<(unsigned)(p.batch * p.heads * p.nsweeps * per), kThr, 0, stream>>>(p, per);
+    linattn_carry_kernel<<<(unsigned)(p.batch * p.heads * p.nsweeps * per), kThr, 0, stream>>>(
+        p, (unsigned)per);
     return cudaGetLastError();
 }
 

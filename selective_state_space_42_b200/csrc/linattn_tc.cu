@@ -54,29 +54,29 @@ struct TcMaps {
 };
 
 // ---- tensor memory -------------------------------------------------------------
-// 16 consecutive columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 8 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          "=r"(r[7])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[k]);
 }
-// The same of two column ranges at once.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16],
-                                            float (&b)[16]) {
+// 16 lanes × 32 columns of two column ranges at once, in fragments: thread t
+// holds, for the c-th 8 columns, lane t/4 columns 2·(t%4), + 1 in v[4c], v[4c+1]
+// and lane t/4 + 8 in v[4c+2], v[4c+3].
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t ta, uint32_t tb, float (&a)[16],
+                                              float (&b)[16]) {
     uint32_t r[32];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
         "[%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
@@ -94,11 +94,34 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)
         b[k] = __uint_as_float(r[16 + k]);
     }
 }
-// 8 columns of this thread's lane (completed by tmem_st_wait).
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+// 16 lanes × 16 columns from fragments: lane t/4 column 4c + t%4 in r[2c], lane
+// t/4 + 8 in r[2c+1] (completed by tmem_st_wait).
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
                    "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four transposed 8×8 matrices of 16-bit elements from / to shared memory;
+// thread t gives the address of row t%8 of matrix t/8.
+__device__ __forceinline__ void ldmatrix_t(const void *row, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_addr(row))
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix_t(void *row, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(smem_addr(row)), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// 4 columns of this thread's lane (completed by tmem_st_wait).
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
@@ -171,49 +194,37 @@ __device__ __forceinline__ uint32_t tile_off(int j, int d) {
 }
 
 // ---- sizes -------------------------------------------------------------------------
-// Tensor-memory columns.
-template <int D, bool kBwd> struct Cols {
-    static constexpr uint32_t S = 0, Yi = 64, Ye = 128, U = 192;
-    static constexpr uint32_t St = U + D, StParts = kBwd ? 2 : 1;
-    static constexpr uint32_t Vp = St + StParts * (D / 2), VpParts = kBwd ? 2 : 3;
-    static_assert(Vp + VpParts * 32 <= 512, "tensor memory");
+// Tensor-memory columns. The pass over the segments' own states holds U and
+// c ◦ V twice instead of the rest.
+template <int D, bool kBwd, bool kFull> struct Cols {
+    static constexpr uint32_t S = 0, Yi = 64, Ye = 128, U = kFull ? 192 : 0;
+    static constexpr uint32_t St = 192 + D, StParts = kBwd ? 2 : 1;
+    static constexpr uint32_t VpParts = kBwd ? 2 : 3;
+    static constexpr uint32_t Vp = kFull ? St + StParts * (D / 2) : 2 * D;
+    static constexpr uint32_t VpNext = VpParts * 32, Bufs = kFull ? 1 : 2;
+    static_assert(Vp + Bufs * VpNext <= 512, "tensor memory");
 };
 
-template <int D, bool kBwd> struct TcSmem {
-    static constexpr int kTiles = kBwd ? 4 : 3;  // q, k, v (, dot)
-    static constexpr int kStages = 3;
+template <int D, bool kBwd, bool kFull> struct TcSmem {
+    static constexpr int kTiles = !kFull ? 2 : kBwd ? 4 : 3;  // (q,) k, v (, dot)
+    static constexpr int kK = kFull ? 1 : 0, kV = kK + 1;     // places of k and v
+    static constexpr int kStages = kFull ? 3 : 6;
     bf16 tile[kStages][kTiles][kC * D];
-    bf16 P[kC * kC];
-    bf16 out[kC * D];               // y on its way out: slabs of 64 columns
+    bf16 P[kFull ? kC * kC : 8];
+    bf16 out[kFull ? kC * D : 8];   // y on its way out: swizzled slabs of 64 columns
     float G[kSlots][kC];            // prefix sums of the log decays times log2 e
     float rowf[kSlots][kC], colw[kSlots][kC];
     float decay[kSlots];
     int reset[kSlots];              // a factor in rowf is zero
     float red[4][kC];
-    uint64_t full[kStages], empty[kStages];
-    uint64_t s_full, s_empty, p_full, p_empty, vp_full, u_full, u_empty, st_full, st_empty;
+    uint64_t full[kStages], empty[kStages], factors[kSlots];
+    uint64_t vp_full[2], u_full[2], u_empty[2];
+    uint64_t s_full, s_empty, p_full, p_empty, st_full, st_empty;
     uint64_t o_full, o_empty, drain;
-    uint64_t v_sync, o_sync;        // the c ◦ V warps, the output warps
+    uint64_t v_sync[2], o_sync;     // the warps of c ◦ V, the output warps
     uint32_t tmem;
     int abort;
 };
-
-// One value per token for this lane (v[i], i = 0 .. 15) -> the sum over the
-// warp's lanes of v[lane mod 16] in lane `lane`: halves are exchanged and added.
-__device__ __forceinline__ float lanes_sum16(float (&v)[16]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int m = 8; m > 0; m >>= 1) {
-        const bool up = (lane & m) != 0;
-#pragma unroll
-        for (int k = 0; k < m; ++k) {
-            const float send = up ? v[k] : v[k + m];
-            const float keep = up ? v[k + m] : v[k];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
-    }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
-}
 
 // 32 columns of row r of P as packed bfloat16: scores times p·2^(G_r − G_j)
 // (reverse: p·2^(G_j − G_r)), zero outside columns lo .. hi. gr = G_r + log2 |p|
@@ -238,52 +249,83 @@ __device__ __forceinline__ void score_weights(const float (&v)[32], const float 
     }
 }
 
-// A chunk's outputs y = Yi + r ◦ Ye of value column d (this thread's lane) into
-// the staging rows (kF32: to float32 rows in memory, nl of them), and with kDot
-// the products with the dot operand summed over the warp's columns. kReset: a
-// factor r of zero is a reset, and Ye does not count whatever it is. Rows
-// behind the sequence's length come out zero (their operands are zero). Token
-// pairs are rounded together.
-template <int D, bool kBwd, bool kF32, bool kDot, bool kReset>
-__device__ __forceinline__ void output_rows(TcSmem<D, kBwd> &S, uint32_t tmem, int s,
-                                            const float *rowf, int d, float *y, long long y_row,
-                                            int nl) {
-    typedef Cols<D, kBwd> C;
-    char *out = reinterpret_cast<char *>(S.out) + (d >> 6) * (kC * 128) + (d & 63) * 2;
-    const char *dot = reinterpret_cast<const char *>(S.tile[s][TcSmem<D, kBwd>::kTiles - 1]);
-    const int lane = threadIdx.x & 31;
+// A chunk's outputs y = Yi + r ◦ Ye of 32 value columns from d0 on (this warp's
+// lanes) into the staging rows (kF32: to float32 rows in memory, nl of them of dv
+// columns), and with kDot the products with the dot operand summed over the
+// columns. kReset: a factor r of zero is a reset, and Ye does not count whatever
+// it is. Rows behind the sequence's length come out zero (their operands are
+// zero). In fragments, so that the transposition to token rows is stmatrix's,
+// and a sum over 32 columns is four additions and a third of a shuffle per
+// token (lane = column took 720 instructions a chunk, and 6.0 µs with the dot
+// products instead of 2.2).
+template <bool kF32, bool kDot, bool kReset>
+__device__ __forceinline__ void output_rows(uint32_t t_yi, uint32_t t_ye, bf16 *out,
+                                            const bf16 *dot, float *red, const float *rowf, int d0,
+                                            float *y, long long y_row, int nl, int dv) {
+    const int t = threadIdx.x & 31, r = t >> 2, c2 = 2 * (t & 3);
+    char *orow = reinterpret_cast<char *>(out);
+    const char *drow = reinterpret_cast<const char *>(dot);
 #pragma unroll 1
-    for (int j0 = 0; j0 < kC; j0 += 16) {
-        float yi[16], ye[16];
-        tmem_ld16x2(tmem + C::Yi + j0, tmem + C::Ye + j0, yi, ye);
+    for (int th = 0; th < 2; ++th) {
+        float acc[8];
 #pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-            const float4 f4 = *reinterpret_cast<const float4 *>(rowf + j0 + 4 * e4);
-            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t at = ((uint32_t)(16 * hh) << 16) + 32 * th;
+            float yi[16], ye[16];
+            tmem_ld_frag2(t_yi + at, t_ye + at, yi, ye);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 4 * e4 + e;
-                yi[k] = kReset && f[e] == 0.f ? yi[k] : fmaf(f[e], ye[k], yi[k]);
+            for (int c = 0; c < 4; ++c) {
+                const float2 f = *reinterpret_cast<const float2 *>(rowf + 32 * th + 8 * c + c2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float g = k & 1 ? f.y : f.x;
+                    const int e = 4 * c + k;
+                    yi[e] = kReset && g == 0.f ? yi[e] : fmaf(g, ye[e], yi[e]);
+                }
             }
-        }
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
             if (kF32) {
-                if (y && j0 + k < nl) y[(j0 + k) * y_row] = yi[k];
-                if (y && j0 + k + 1 < nl) y[(j0 + k + 1) * y_row] = yi[k + 1];
-            } else {
-                const uint32_t u = pack_bf16x2(yi[k], yi[k + 1]);
-                *reinterpret_cast<uint16_t *>(out + (j0 + k) * 128) = (uint16_t)u;
-                *reinterpret_cast<uint16_t *>(out + (j0 + k) * 128 + 128) = (uint16_t)(u >> 16);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = 32 * th + 8 * (e >> 2) + c2 + (e & 1);
+                    const int d = d0 + 16 * hh + r + 8 * ((e >> 1) & 1);
+                    if (j < nl && d < dv) y[j * y_row + d] = yi[e];
+                }
+            }
+#pragma unroll
+            for (int cp = 0; cp < 2; ++cp) {
+                const uint32_t off = tile_off(32 * th + 16 * cp + 8 * (t >> 4) + (t & 7),
+                                              d0 + 16 * hh + (t & 8));
+                const float *v = yi + 8 * cp;
+                if (!kF32)
+                    stmatrix_t(orow + off, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                if (kDot) {
+                    uint32_t q[4];
+                    ldmatrix_t(drow + off, q);
+                    float *s = acc + 4 * cp;
+                    s[0] = fmaf(v[0], bf_lo(q[0]), fmaf(v[2], bf_lo(q[1]), s[0]));
+                    s[1] = fmaf(v[1], bf_hi(q[0]), fmaf(v[3], bf_hi(q[1]), s[1]));
+                    s[2] = fmaf(v[4], bf_lo(q[2]), fmaf(v[6], bf_lo(q[3]), s[2]));
+                    s[3] = fmaf(v[5], bf_hi(q[2]), fmaf(v[7], bf_hi(q[3]), s[3]));
+                }
             }
         }
         if (kDot) {
+            // over the 8 lanes of a column group: halves are exchanged and added,
+            // lane group r keeps token 8·(r / 2) + c2 + r % 2
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                yi[k] *= __bfloat162float(
-                    *reinterpret_cast<const bf16 *>(dot + j0 * 128 + tile_off(k, d)));
-            const float sum = lanes_sum16(yi);
-            if (lane < 16) S.red[(threadIdx.x >> 5) & 3][j0 + lane] = sum;
+            for (int m = 4; m > 0; m >>= 1) {
+                const bool up = (r & m) != 0;
+#pragma unroll
+                for (int k = 0; k < m; ++k) {
+                    const float send = up ? acc[k] : acc[k + m];
+                    const float keep = up ? acc[k + m] : acc[k];
+                    acc[k] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * m);
+                }
+            }
+            red[32 * th + 8 * (r >> 1) + c2 + (r & 1)] = acc[0];
         }
     }
 }
@@ -293,8 +335,8 @@ __device__ __forceinline__ void output_rows(TcSmem<D, kBwd> &S, uint32_t tmem, i
 template <int D, bool kBwd, bool kFull>
 __global__ void __launch_bounds__(kThr, 1)
 linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant__ TcMaps maps) {
-    typedef TcSmem<D, kBwd> Smem;
-    typedef Cols<D, kBwd> C;
+    typedef TcSmem<D, kBwd, kFull> Smem;
+    typedef Cols<D, kBwd, kFull> C;
     constexpr int kStages = Smem::kStages;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
@@ -326,15 +368,18 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         mbar_init(&S.s_empty, 2);
         mbar_init(&S.p_full, 2);
         mbar_init(&S.p_empty, 1);
-        mbar_init(&S.vp_full, 4);
-        mbar_init(&S.u_full, 1);
-        mbar_init(&S.u_empty, 8);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&S.vp_full[k], 4);
+            mbar_init(&S.u_full[k], 1);
+            mbar_init(&S.u_empty[k], 8);
+            mbar_init(&S.v_sync[k], 4);
+        }
+        for (int k = 0; k < kSlots; ++k) mbar_init(&S.factors[k], 1);
         mbar_init(&S.st_full, 8);
         mbar_init(&S.st_empty, 1);
         mbar_init(&S.o_full, 1);
         mbar_init(&S.o_empty, 4);
         mbar_init(&S.drain, 1);
-        mbar_init(&S.v_sync, 4);
         mbar_init(&S.o_sync, 4);
         S.abort = 0;
         fence_barrier_init();
@@ -354,8 +399,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     };
     bool ok = true;
     // Chunk i's factors stand in slot i % kSlots. The producer runs at most
-    // kStages chunks ahead of the MMAs, every reader of chunk i is done before
-    // the MMAs of chunk i + 2, so eight slots need no barrier of their own.
+    // kStages (≤ 6) chunks ahead of the MMAs and every reader of chunk i is done
+    // before the MMAs of chunk i + 2 end, so a slot is free when its turn comes.
+    // Roles that hold no stage wait for the slot's barrier: a stage's could be two
+    // phases on by then.
+    constexpr int kBufs = (int)C::Bufs;
     if (warp < 4) {
     if (warp == kWarpTma) {
         // ---- producer: tiles by TMA, decays by the warp -----------------------------
@@ -388,8 +436,10 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 for (int sl = 0; sl < kSlabs; ++sl) {
                     if (kFull)
                         tma_load_4d(&S.tile[s][0][sl * kC * 64], mq, &S.full[s], sl * 64, hq, t0, b);
-                    tma_load_4d(&S.tile[s][1][sl * kC * 64], mk, &S.full[s], sl * 64, hk, t0, b);
-                    tma_load_4d(&S.tile[s][2][sl * kC * 64], mv, &S.full[s], sl * 64, hv, t0, b);
+                    tma_load_4d(&S.tile[s][Smem::kK][sl * kC * 64], mk, &S.full[s], sl * 64, hk, t0,
+                                b);
+                    tma_load_4d(&S.tile[s][Smem::kV][sl * kC * 64], mv, &S.full[s], sl * 64, hv, t0,
+                                b);
                     if (has_dot)
                         tma_load_4d(&S.tile[s][Smem::kTiles - 1][sl * kC * 64], md, &S.full[s],
                                     sl * 64, hd, t0, b);
@@ -429,6 +479,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             if (lane == 0) S.reset[sl] = reset;
             seg_log2 += end;
             arrive(&S.full[s]);
+            if (lane == 0) mbar_arrive(&S.factors[sl]);
         }
         if (!kFull && lane == 0)
             a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
@@ -458,7 +509,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
             const int s = i % kStages;
             if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
-            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]);
+            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][Smem::kK]);
             if (lane == 0) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
@@ -470,20 +521,22 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         if (kFull && n > 0) scores(0);
         for (int i = 0; ok && i < n; ++i) {
             const int s = i % kStages;
-            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][1]),
-                           v = smem_addr(S.tile[s][2]);
+            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][Smem::kK]),
+                           v = smem_addr(S.tile[s][Smem::kV]);
+            const int buf = i % kBufs, use = i / kBufs;
             // U: both operands' K is the token (16 tokens = two 8-row atoms of a slab). Its
             // tiles have landed: c ◦ V was made from them.
-            if (!wait2(&S.vp_full, i, &S.u_empty, (i & 1) ^ 1)) break;
+            if (!wait2(&S.vp_full[buf], use, &S.u_empty[buf], (use & 1) ^ 1)) break;
             if (lane == 0) {
 #pragma unroll
                 for (int part = 0; part < (int)C::VpParts; ++part)
 #pragma unroll
                     for (int x = 0; x < kC / 16; ++x)
-                        umma_bf16_ts(tmem + C::U, tmem + C::Vp + part * 32 + x * 8,
+                        umma_bf16_ts(tmem + C::U + buf * D,
+                                     tmem + C::Vp + buf * C::VpNext + part * 32 + x * 8,
                                      umma_desc_sw128(k + x * 2048, kSlab, 1024), id_u,
                                      part > 0 || x > 0);
-                umma_commit(&S.u_full);
+                umma_commit(&S.u_full[buf]);
                 if (!kFull) umma_commit(&S.empty[s]);
             }
             __syncwarp();
@@ -574,69 +627,77 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             }
         }
     }
-    } else if (warp < 8) {
+    } else if (warp < 8 || (!kFull && warp >= 16)) {
         // ---- c ◦ V as bfloat16 parts, column d of V on lane d --------------------------
-        const int d = 32 * (warp & 3) + lane;
+        // In the pass over the segments' own states the output warps take every other chunk.
+        const int group = warp >= 16 ? 1 : 0, tg = t - (group ? 512 : 128);
+        const int d0 = 32 * (warp & 3), r8 = lane >> 4, c2 = 2 * (lane & 3);
         uint32_t syncs = 0;
-        for (int i = 0; i < n; ++i) {
-            const int s = i % kStages;
+        for (int i = group; i < n; i += kBufs) {
+            const int s = i % kStages, buf = i % kBufs, use = i / kBufs;
             const int nq = min(kC, len - chunk_of(i) * kC);
             ok = wait(&S.full[s], i / kStages);
             if (!ok) break;
             if (nq < kC && len < p.seqlen) {
                 // what stands behind the row's length may be anything: zero it
-                for (int e = t - 128; e < (kC - nq) * (D / 8); e += 128) {
+                for (int e = tg; e < (kC - nq) * (D / 8); e += 128) {
                     const uint32_t off = tile_off(nq + e / (D / 8), 8 * (e % (D / 8)));
 #pragma unroll 1
-                    for (int x = kFull ? 0 : 1; x < Smem::kTiles; ++x)
+                    for (int x = 0; x < Smem::kTiles; ++x)
                         *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(S.tile[s][x]) + off) =
                             make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
-                arrive(&S.v_sync);
-                ok = wait(&S.v_sync, syncs++);
+                arrive(&S.v_sync[group]);
+                ok = wait(&S.v_sync[group], syncs++);
                 if (!ok) break;
             }
-            if (i > 0) {
-                ok = wait(&S.u_full, (i - 1) & 1);  // U has read the previous parts
+            if (use > 0) {
+                ok = wait(&S.u_full[buf], use - 1);  // U has read the previous parts
                 if (!ok) break;
                 tc_fence_after();
             }
-            if (d < D) {
-                const char *tile = reinterpret_cast<const char *>(S.tile[s][2]);
+            if (d0 < D) {
+                const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
+                const float *w = S.colw[i % kSlots];
+                const uint32_t at = tmem + lanes + C::Vp + buf * C::VpNext;
                 // rolled: the loop bodies of the five roles share the instruction caches
 #pragma unroll 1
-                for (int j16 = 0; j16 < kC / 16; ++j16) {
+                for (int q = 0; q < 4; ++q) {  // 32 tokens × 16 columns
+                    const int th = q >> 1, hh = q & 1;
                     uint32_t part[3][8];
 #pragma unroll
-                    for (int e2 = 0; e2 < 8; ++e2) {
-                        const int j = 2 * e2;  // of the 16 tokens (the swizzle's period is 8)
-                        const float2 w =
-                            *reinterpret_cast<const float2 *>(&S.colw[i % kSlots][16 * j16 + j]);
-                        float x0 = w.x * __bfloat162float(*reinterpret_cast<const bf16 *>(
-                                             tile + 2048 * j16 + tile_off(j, d)));
-                        float x1 = w.y * __bfloat162float(*reinterpret_cast<const bf16 *>(
-                                             tile + 2048 * j16 + tile_off(j + 1, d)));
+                    for (int cp = 0; cp < 2; ++cp) {
+                        uint32_t v[4];
+                        ldmatrix_t(tile + tile_off(32 * th + 16 * cp + 8 * r8 + (lane & 7),
+                                                   d0 + 16 * hh + (lane & 8)),
+                                   v);
 #pragma unroll
-                        for (int k = 0; k < (int)C::VpParts; ++k) {
-                            // all parts but the last by truncation (no conversion)
-                            const uint32_t u =
-                                k + 1 < (int)C::VpParts
-                                    ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
-                                    : pack_bf16x2(x0, x1);
-                            part[k][e2] = u;
-                            x0 -= __uint_as_float(u << 16);
-                            x1 -= __uint_as_float(u & 0xFFFF0000u);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = *reinterpret_cast<const float2 *>(
+                                w + 32 * th + 16 * cp + 8 * (k >> 1) + c2);
+                            float x0 = f.x * bf_lo(v[k]), x1 = f.y * bf_hi(v[k]);
+#pragma unroll
+                            for (int e = 0; e < (int)C::VpParts; ++e) {
+                                // all parts but the last by truncation (no conversion)
+                                const uint32_t u =
+                                    e + 1 < (int)C::VpParts
+                                        ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
+                                        : pack_bf16x2(x0, x1);
+                                part[e][4 * cp + k] = u;
+                                x0 -= bf_lo(u);
+                                x1 -= bf_hi(u);
+                            }
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < (int)C::VpParts; ++k)
-                        tmem_st8(tmem + lanes + C::Vp + k * 32 + 8 * j16, part[k]);
+                    for (int e = 0; e < (int)C::VpParts; ++e)
+                        tmem_st_frag(at + ((uint32_t)(16 * hh) << 16) + e * 32 + 16 * th, part[e]);
                 }
                 tmem_st_wait();
             }
             tc_fence_before();
-            arrive(&S.vp_full);
+            arrive(&S.vp_full[buf]);
         }
     } else if (warp < 16) {
         // ---- state: lane d, columns half·D/2 .. ------------------------------------------
@@ -653,60 +714,57 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 src = a.h_init + bh * elems;
                 tr = a.h_init_t != 0;
             }
+            const int step = tr ? 1 : a.dv, cols = src && d < a.dv ? a.dk - half * kH : 0;
+            if (src) src += (tr ? d * a.dk : d) + half * kH * step;
 #pragma unroll
-            for (int k = 0; k < kH; ++k) {
-                const int c = half * kH + k;
-                st[k] = src && d < a.dv && c < a.dk
-                            ? src[tr ? (long long)d * a.dk + c : (long long)c * a.dv + d] : 0.f;
-            }
+            for (int k = 0; k < kH; ++k) st[k] = k < cols ? src[k * step] : 0.f;
         }
         for (int i = 0; i < n; ++i) {
-            const int s = i % kStages;
+            const int buf = i % kBufs, use = i / kBufs;
             if (kFull) {
                 ok = wait(&S.st_empty, (i & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (d < D) {
 #pragma unroll
-                    for (int k16 = 0; k16 < kH / 16; ++k16) {
-                        uint32_t hi[8], lo[8];
+                    for (int k8 = 0; k8 < kH / 8; ++k8) {
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x0 = st[16 * k16 + 2 * e], x1 = st[16 * k16 + 2 * e + 1];
+                        for (int e = 0; e < 4; ++e) {
+                            const float x0 = st[8 * k8 + 2 * e], x1 = st[8 * k8 + 2 * e + 1];
                             hi[e] = pack_bf16x2(x0, x1);
-                            lo[e] = pack_bf16x2(x0 - __uint_as_float(hi[e] << 16),
-                                                x1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+                            if (kBwd) lo[e] = pack_bf16x2(x0 - bf_lo(hi[e]), x1 - bf_hi(hi[e]));
                         }
-                        const uint32_t at = tmem + lanes + C::St + half * (kH / 2) + 8 * k16;
-                        tmem_st8(at, hi);
-                        if (kBwd) tmem_st8(at + D / 2, lo);
+                        const uint32_t at = tmem + lanes + C::St + half * (kH / 2) + 4 * k8;
+                        tmem_st4(at, hi);
+                        if (kBwd) tmem_st4(at + D / 2, lo);
                     }
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 arrive(&S.st_full);
             }
-            ok = wait(&S.full[s], i / kStages) && wait(&S.u_full, i & 1);
+            ok = wait(&S.factors[i % kSlots], i / kSlots) && wait(&S.u_full[buf], use);
             if (!ok) break;
             tc_fence_after();
             const float dec = S.decay[i % kSlots];
             if (d < D) {
 #pragma unroll
-                for (int k16 = 0; k16 < kH / 16; ++k16) {
-                    float u[16];
-                    tmem_ld16(tmem + lanes + C::U + half * kH + 16 * k16, u);
+                for (int k8 = 0; k8 < kH / 8; ++k8) {
+                    float u[8];
+                    tmem_ld8(tmem + lanes + C::U + buf * D + half * kH + 8 * k8, u);
                     if (dec == 0.f) {  // a reset: the old state does not count
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) st[16 * k16 + e] = u[e];
+                        for (int e = 0; e < 8; ++e) st[8 * k8 + e] = u[e];
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            st[16 * k16 + e] = fmaf(dec, st[16 * k16 + e], u[e]);
+                        for (int e = 0; e < 8; ++e)
+                            st[8 * k8 + e] = fmaf(dec, st[8 * k8 + e], u[e]);
                     }
                 }
             }
             tc_fence_before();
-            arrive(&S.u_empty);
+            arrive(&S.u_empty[buf]);
         }
         float *dst = nullptr;
         bool tr = false;
@@ -716,17 +774,17 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             dst = a.h_final + bh * elems;
             tr = a.h_final_t != 0;
         }
-        if (dst && d < a.dv) {
+        if (dst) {
+            const int step = tr ? 1 : a.dv, cols = d < a.dv ? a.dk - half * kH : 0;
+            dst += (tr ? d * a.dk : d) + half * kH * step;
 #pragma unroll
-            for (int k = 0; k < kH; ++k) {
-                const int c = half * kH + k;
-                if (c < a.dk) dst[tr ? (long long)d * a.dk + c : (long long)c * a.dv + d] = st[k];
-            }
+            for (int k = 0; k < kH; ++k)
+                if (k < cols) dst[k * step] = st[k];
         }
     } else {
         if (kFull) {
         // ---- outputs: lane d, a column per token -----------------------------------------
-        const int d = 32 * (warp & 3) + lane;
+        const int d0 = 32 * (warp & 3);
         const int tl = t - 512;  // 0 .. 127
         const CUtensorMap *my = &maps.m[a.map_y];
         const bool f32 = kBwd && a.y_f32;
@@ -734,30 +792,30 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         for (int i = 0; i < n; ++i) {
             const int s = i % kStages;
             const int t0 = chunk_of(i) * kC, nq = min(kC, len - t0);
-            ok = wait(&S.full[s], i / kStages) && wait(&S.o_full, i & 1);
+            ok = wait(&S.factors[i % kSlots], i / kSlots) && wait(&S.o_full, i);
             if (!ok) break;
             tc_fence_after();
             if (tl == 0) bulk_wait_read<0>();  // the previous chunk's store has read the staging
             arrive(&S.o_sync);
             ok = wait(&S.o_sync, syncs++);
             if (!ok) break;
-            if (d < D) {
+            if (d0 < D) {
                 // float32 rows (the heads' parts of a shared gradient) go straight to memory
                 const int nl = (int)min((long long)kC, p.seqlen - t0);
                 const long long y_row = (long long)p.heads * a.dv;
-                float *yf = f32 && d < a.dv
-                                ? static_cast<float *>(a.y) +
-                                      ((long long)b * p.seqlen + t0) * y_row + h * a.dv + d
+                float *yf = f32 ? static_cast<float *>(a.y) +
+                                      ((long long)b * p.seqlen + t0) * y_row + h * a.dv
                                 : nullptr;
-                const uint32_t at = tmem + lanes;
-                const float *rowf = S.rowf[i % kSlots];
+                const bf16 *dot = S.tile[s][Smem::kTiles - 1];
                 auto rows = [&](auto is_f32, auto is_dot) {
                     if (S.reset[i % kSlots])
-                        output_rows<D, kBwd, decltype(is_f32)::value, decltype(is_dot)::value, true>(
-                            S, at, s, rowf, d, yf, y_row, nl);
+                        output_rows<decltype(is_f32)::value, decltype(is_dot)::value, true>(
+                            tmem + lanes + C::Yi, tmem + lanes + C::Ye, S.out, dot,
+                            S.red[warp & 3], S.rowf[i % kSlots], d0, yf, y_row, nl, a.dv);
                     else
-                        output_rows<D, kBwd, decltype(is_f32)::value, decltype(is_dot)::value, false>(
-                            S, at, s, rowf, d, yf, y_row, nl);
+                        output_rows<decltype(is_f32)::value, decltype(is_dot)::value, false>(
+                            tmem + lanes + C::Yi, tmem + lanes + C::Ye, S.out, dot,
+                            S.red[warp & 3], S.rowf[i % kSlots], d0, yf, y_row, nl, a.dv);
                 };
                 if constexpr (kBwd) {
                     if (has_dot && f32)
@@ -819,7 +877,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
 // [batch][seqlen][heads][dim] with `row` elements between tokens: boxes of 64
 // tokens and 64 columns.
 bool make_map(CUtensorMap *m, const void *base, long long batch, long long seqlen, int heads,
-              int dim, long long row, bool swizzle) {
+              int dim, long long row) {
     auto fn = tma_encode();
     if (!fn) return false;
     cuuint64_t gdim[4] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)seqlen, (cuuint64_t)batch};
@@ -828,23 +886,23 @@ bool make_map(CUtensorMap *m, const void *base, long long batch, long long seqle
     cuuint32_t box[4] = {64, 1, (cuuint32_t)kC, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim, gstride, box,
-              estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool kBwd>
 cudaError_t launch(const LinattnParams &p, const TcMaps &maps, cudaStream_t stream) {
-    const int smem = (int)sizeof(TcSmem<D, kBwd>) + 1024;
+    const int smem = (int)sizeof(TcSmem<D, kBwd, true>) + 1024;
+    const int smem_own = (int)sizeof(TcSmem<D, kBwd, false>) + 1024;
     auto full = linattn_tc_kernel<D, kBwd, true>;
     auto state = linattn_tc_kernel<D, kBwd, false>;
     cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_own);
     if (e != cudaSuccess) return e;
     const long long per_seg = p.batch * p.heads * p.nsweeps;
     if (p.nseg > 1) {
-        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem, stream>>>(p, maps);
+        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem_own, stream>>>(p, maps);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
         if (e != cudaSuccess) return e;
@@ -876,7 +934,7 @@ cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) 
             if (keys[i].ptr == ptr && keys[i].row == row && keys[i].dim == dim &&
                 keys[i].heads == heads)
                 return i;
-        if (n >= kMaps || !make_map(&maps.m[n], ptr, p.batch, p.seqlen, heads, dim, row, true))
+        if (n >= kMaps || !make_map(&maps.m[n], ptr, p.batch, p.seqlen, heads, dim, row))
             return -1;
         keys[n] = Key{ptr, row, dim, heads};
         return n++;
@@ -895,7 +953,7 @@ cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) 
         SweepArgs &a = p.sweep[s];
         if (a.y_f32) continue;  // stored without TMA
         if (n >= kMaps || !make_map(&maps.m[n], a.y, p.batch, p.seqlen, p.heads, a.dv,
-                                    (long long)p.heads * a.dv, false))
+                                    (long long)p.heads * a.dv))
             return cudaErrorInvalidValue;
         keys[n] = Key{nullptr, 0, 0, 0};
         a.map_y = n++;

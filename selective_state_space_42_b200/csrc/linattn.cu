@@ -406,29 +406,57 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
 }
 
 // seg_state[s]: the segment's own state -> the state entering it, in the
-// sweep's order. One thread per state element.
+// sweep's order. A thread carries kV neighbouring elements; eight segments'
+// loads are in flight before the first is used.
+template <int kV>
 __global__ void __launch_bounds__(kThr)
 linattn_carry_kernel(const __grid_constant__ LinattnParams p, unsigned blocks_per) {
+    constexpr int kAhead = 8;
     const unsigned id = blockIdx.x / blocks_per;
     const SweepArgs &a = p.sweep[id % (unsigned)p.nsweeps];
     const long long bh = id / (unsigned)p.nsweeps;
     const int n = a.dk * a.dv;
-    const int e = (int)(blockIdx.x % blocks_per) * kThr + (int)threadIdx.x;
-    if (e >= n) return;
-    float h = 0.f;
-    if (a.h_init)
-        h = a.h_init[bh * n + (a.h_init_t ? (e % a.dv) * a.dk + e / a.dv : e)];
-#pragma unroll 4
-    for (int o = 0; o < p.nseg; ++o) {
-        const int s = a.reverse ? p.nseg - 1 - o : o;
-        float *x = a.seg_state + (bh * p.nseg + s) * n + e;
-        if (o + 1 < p.nseg) {
-            const float own = *x;
-            *x = h;
-            const float dec = __ldg(a.seg_decay + bh * p.nseg + s);
-            h = dec == 0.f ? own : fmaf(dec, h, own);
-        } else {
-            *x = h;
+    const int e0 = ((int)(blockIdx.x % blocks_per) * kThr + (int)threadIdx.x) * kV;
+    if (e0 >= n) return;
+    float h[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int e = e0 + v;
+        h[v] = a.h_init ? a.h_init[bh * n + (a.h_init_t ? (e % a.dv) * a.dk + e / a.dv : e)] : 0.f;
+    }
+    float *base = a.seg_state + bh * p.nseg * n + e0;
+    const float *decay = a.seg_decay + bh * p.nseg;
+    for (int o0 = 0; o0 < p.nseg; o0 += kAhead) {
+        float own[kAhead][kV], dec[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int o = o0 + k, s = a.reverse ? p.nseg - 1 - o : o;
+            if (o + 1 >= p.nseg) continue;  // the last segment's own state is not made
+            dec[k] = __ldg(decay + s);
+            if (kV == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(base + (long long)s * n);
+                own[k][0] = f.x;
+                own[k][kV > 1 ? 1 : 0] = f.y;
+                own[k][kV > 2 ? 2 : 0] = f.z;
+                own[k][kV > 3 ? 3 : 0] = f.w;
+            } else {
+                own[k][0] = base[(long long)s * n];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int o = o0 + k, s = a.reverse ? p.nseg - 1 - o : o;
+            if (o >= p.nseg) break;
+            float *x = base + (long long)s * n;
+            if (kV == 4)
+                *reinterpret_cast<float4 *>(x) = make_float4(h[0], h[kV > 1 ? 1 : 0],
+                                                             h[kV > 2 ? 2 : 0], h[kV > 3 ? 3 : 0]);
+            else
+                *x = h[0];
+            if (o + 1 >= p.nseg) break;
+#pragma unroll
+            for (int v = 0; v < kV; ++v)  // a decay of zero is a reset
+                h[v] = dec[k] == 0.f ? own[k][v] : fmaf(dec[k], h[v], own[k][v]);
         }
     }
 }
@@ -590,10 +618,14 @@ cudaError_t launch_linattn_sweeps(const LinattnParams &p, bool bf16, cudaStream_
 }
 
 cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream) {
-    const long long n = (long long)p.sweep[0].dk * p.sweep[0].dv;  // the same for every sweep
-    const long long per = (n + kThr - 1) / kThr;
-    linattn_carry_kernel<<<(unsigned)(p.batch * p.heads * p.nsweeps * per), kThr, 0, stream>>>(
-        p, (unsigned)per);
+    const int n = p.sweep[0].dk * p.sweep[0].dv;  // the same for every sweep
+    const int v = n % 4 == 0 ? 4 : 1;
+    const unsigned per = (unsigned)((n / v + kThr - 1) / kThr);
+    const unsigned blocks = (unsigned)(p.batch * p.heads * p.nsweeps) * per;
+    if (v == 4)
+        linattn_carry_kernel<4><<<blocks, kThr, 0, stream>>>(p, per);
+    else
+        linattn_carry_kernel<1><<<blocks, kThr, 0, stream>>>(p, per);
     return cudaGetLastError();
 }
 

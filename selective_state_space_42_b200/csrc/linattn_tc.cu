@@ -4,15 +4,21 @@
 //
 // Per (batch row, head), chunks of 64 tokens (formulas in linattn.cu). The
 // state S is held transposed, value column d on tensor-memory lane d:
-//   scores   A = Q Kᵀ                       64 (of 128) × 64 × D
-//   Yi       (P V)ᵀ = Vᵀ Pᵀ, P = A ◦ weights     128 × 64 × 64
-//   Ye       (Q S_in)ᵀ = S_inᵀ Qᵀ           128 × 64 × D
+//   scores   Q Kᵀ                           64 (of 128) × 64 × D
+//   Y        (Q S_in)ᵀ = S_inᵀ Qᵀ           128 × 64 × D, and on top of it
+//            (P V)ᵀ = Vᵀ Pᵀ                 128 × 64 × 64
 //   U        Σ_j c_j·v_j k_jᵀ = (c ◦ V)ᵀ K  128 × D × 64
-//   y = Yi + r_i·Ye,   S ← exp(G_end)·S + U
+//   y = r ◦ Y,   S ← exp(G_end)·S + U
+// A pair's weight exp(A_row − A_col) is split: P takes 1/exp(A_col), the output
+// r = exp(A_row), so that P costs a product per score and the two products one
+// accumulator. The gradient keeps the row factor in P and the products apart: its
+// sweeps for dq and dk must round the same weights the same way (their dot
+// products cancel in the log decays' gradient). So does, with an exponential per
+// score, a chunk whose factors leave 2^±60 (a reset, a few tokens of strong decay).
 // Q, K, V (and in the gradient the operand of the dot product) come by TMA into
 // a ring of stages, 128-byte swizzled; P is written to shared memory; S_in and
 // c ◦ V are A operands in tensor memory. Warps (20, one block an SM):
-//   0-1    P: scores from tensor memory, weights exp(G_i − G_j), to bfloat16
+//   0-1    P: scores from tensor memory, weighted, to bfloat16
 //   2      TMA producer, and each chunk's prefix sums of the log decays
 //   3      issues every MMA (one thread)
 //   4-7    c ◦ V: lane d reads column d of V, scales and splits it
@@ -39,7 +45,7 @@ constexpr int kC = kLaChunk;
 constexpr long long kWaitClocks = 4000000000ll;  // every wait gives up after about 2 s
 constexpr int kStatusLinattnWait = 6;         // device error code
 constexpr int kThr = 640;
-constexpr int kSlots = 8;                     // ring of the chunks' decay factors
+constexpr float kRange = 60.f;                // |log2| a chunk's split factors may reach
 constexpr int kWarpTma = 2, kWarpMma = 3;
 constexpr int kMaps = 8;
 
@@ -67,32 +73,22 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[k]);
 }
-// 16 lanes × 32 columns of two column ranges at once, in fragments: thread t
-// holds, for the c-th 8 columns, lane t/4 columns 2·(t%4), + 1 in v[4c], v[4c+1]
-// and lane t/4 + 8 in v[4c+2], v[4c+3].
-__device__ __forceinline__ void tmem_ld_frag2(uint32_t ta, uint32_t tb, float (&a)[16],
-                                              float (&b)[16]) {
-    uint32_t r[32];
+// 16 lanes × 32 columns in fragments: thread t holds, for the c-th 8 columns,
+// lane t/4 columns 2·(t%4), + 1 in v[4c], v[4c+1] and lane t/4 + 8 in v[4c+2],
+// v[4c+3].
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-        "[%33];\n\t"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(ta), "r"(tb)
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        a[k] = __uint_as_float(r[k]);
-        b[k] = __uint_as_float(r[16 + k]);
-    }
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
 }
 // 16 lanes × 16 columns from fragments: lane t/4 column 4c + t%4 in r[2c], lane
 // t/4 + 8 in r[2c+1] (completed by tmem_st_wait).
@@ -167,6 +163,20 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const i
     return mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity, abort);
 }
 
+// One lane of the warp, always the same. Asked for where it is used, with the warp
+// brought together: kept in a register over divergent code, the answer was
+// measured to be worked out anew there, with two lanes issuing.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---- TMA -------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int c0, int c1, int c2, int c3) {
@@ -209,13 +219,14 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     static constexpr int kTiles = !kFull ? 2 : kBwd ? 4 : 3;  // (q,) k, v (, dot)
     static constexpr int kK = kFull ? 1 : 0, kV = kK + 1;     // places of k and v
     static constexpr int kStages = kFull ? 3 : 6;
+    static constexpr int kSlots = kFull ? 6 : 8;              // ring of the chunks' decay factors
     bf16 tile[kStages][kTiles][kC * D];
     bf16 P[kFull ? kC * kC : 8];
     bf16 out[kFull ? kC * D : 8];   // y on its way out: swizzled slabs of 64 columns
-    float G[kSlots][kC];            // prefix sums of the log decays times log2 e
-    float rowf[kSlots][kC], colw[kSlots][kC];
+    float A[kSlots][kC];            // log2 of the row factors without their scale
+    float rowf[kSlots][kC], colf[kSlots][kC], colw[kSlots][kC];
     float decay[kSlots];
-    int reset[kSlots];              // a factor in rowf is zero
+    int strong[kSlots];             // the factors of P leave float32's comfortable range
     float red[4][kC];
     uint64_t full[kStages], empty[kStages], factors[kSlots];
     uint64_t vp_full[2], u_full[2], u_empty[2];
@@ -226,22 +237,23 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     int abort;
 };
 
-// 32 columns of row r of P as packed bfloat16: scores times p·2^(G_r − G_j)
-// (reverse: p·2^(G_j − G_r)), zero outside columns lo .. hi. gr = G_r + log2 |p|
-// (reverse: G_r − log2 |p|).
-template <bool kRev>
-__device__ __forceinline__ void score_weights(const float (&v)[32], const float *G, float gr,
-                                              int lo, int hi, uint32_t (&out)[16]) {
+// 32 columns of a row of P as packed bfloat16: scores times f_j (kRow: times
+// `row` too); in a strong chunk times row·2^(a − f_j), f the columns' A. Zero
+// outside columns lo .. hi. Selects, not branches.
+template <bool kRow, bool kStrong>
+__device__ __forceinline__ void score_weights(const float (&v)[32], const float *f, float row,
+                                              float a, int lo, int hi, uint32_t (&out)[16]) {
 #pragma unroll
     for (int e4 = 0; e4 < 8; ++e4) {
-        const float4 g4 = *reinterpret_cast<const float4 *>(G + 4 * e4);
-        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+        const float4 f4 = *reinterpret_cast<const float4 *>(f + 4 * e4);
+        const float g[4] = {f4.x, f4.y, f4.z, f4.w};
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // selects, not branches
             const int j = 4 * e4 + e;
-            const float w = v[j] * ex2_approx(kRev ? g[e] - gr : gr - g[e]);
+            float w = kStrong ? ex2_approx(a - g[e]) : g[e];
+            if (kRow || kStrong) w *= row;
+            w *= v[j];
             x[e] = j >= lo && j <= hi ? w : 0.f;
         }
         out[2 * e4] = pack_bf16x2(x[0], x[1]);
@@ -249,66 +261,80 @@ __device__ __forceinline__ void score_weights(const float (&v)[32], const float 
     }
 }
 
-// A chunk's outputs y = Yi + r ◦ Ye of 32 value columns from d0 on (this warp's
-// lanes) into the staging rows (kF32: to float32 rows in memory, nl of them of dv
-// columns), and with kDot the products with the dot operand summed over the
-// columns. kReset: a factor r of zero is a reset, and Ye does not count whatever
-// it is. Rows behind the sequence's length come out zero (their operands are
-// zero). In fragments, so that the transposition to token rows is stmatrix's,
-// and a sum over 32 columns is four additions and a third of a shuffle per
-// token (lane = column took 720 instructions a chunk, and 6.0 µs with the dot
-// products instead of 2.2).
-template <bool kF32, bool kDot, bool kReset>
-__device__ __forceinline__ void output_rows(uint32_t t_yi, uint32_t t_ye, bf16 *out,
+// A chunk's outputs of 32 value columns from d0 on (this warp's lanes): y = r ◦ Y,
+// or Y + r ◦ Ye where the two products are kept apart (kTwo; kReset: where r is
+// zero, a reset, Ye does not count whatever it is). The accumulators are given
+// back (`done`) as soon as the last is read. The outputs go into the staging rows
+// (kF32: to float32 rows in memory, nl of them of dv columns), and with kDot
+// their products with the dot operand, summed over the columns, into `red`. Rows
+// behind the sequence's length come out zero (their operands are zero). In
+// fragments, so that the transposition to token rows is stmatrix's, and a sum
+// over 32 columns is four additions and a ninth of a shuffle per token (with a
+// lane per column a chunk took 720 instructions and 6000 clocks with the dot
+// products).
+template <bool kF32, bool kDot, bool kTwo, bool kReset, typename Done>
+__device__ __forceinline__ void output_rows(uint32_t t_y, uint32_t t_ye, bf16 *out,
                                             const bf16 *dot, float *red, const float *rowf, int d0,
-                                            float *y, long long y_row, int nl, int dv) {
+                                            float *y, long long y_row, int nl, int dv,
+                                            const Done &done) {
     const int t = threadIdx.x & 31, r = t >> 2, c2 = 2 * (t & 3);
     char *orow = reinterpret_cast<char *>(out);
     const char *drow = reinterpret_cast<const char *>(dot);
+    // rolled by 32 tokens: the loop bodies of the five roles share the instruction caches
 #pragma unroll 1
     for (int th = 0; th < 2; ++th) {
-        float acc[8];
+        float v[2][16];  // the warp's two halves of 16 columns
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-#pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
             const uint32_t at = ((uint32_t)(16 * hh) << 16) + 32 * th;
-            float yi[16], ye[16];
-            tmem_ld_frag2(t_yi + at, t_ye + at, yi, ye);
+            tmem_ld_frag(t_y + at, v[hh]);
+            float ye[16];
+            if (kTwo) tmem_ld_frag(t_ye + at, ye);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float2 f = *reinterpret_cast<const float2 *>(rowf + 32 * th + 8 * c + c2);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float g = k & 1 ? f.y : f.x;
-                    const int e = 4 * c + k;
-                    yi[e] = kReset && g == 0.f ? yi[e] : fmaf(g, ye[e], yi[e]);
+                    float &x = v[hh][4 * c + k];
+                    if (!kTwo)
+                        x *= g;
+                    else if (!kReset || g != 0.f)
+                        x = fmaf(g, ye[4 * c + k], x);
                 }
             }
+        }
+        if (th == 1) done();
+        float acc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const float(&x)[16] = v[hh];
             if (kF32) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = 32 * th + 8 * (e >> 2) + c2 + (e & 1);
                     const int d = d0 + 16 * hh + r + 8 * ((e >> 1) & 1);
-                    if (j < nl && d < dv) y[j * y_row + d] = yi[e];
+                    if (j < nl && d < dv) y[j * y_row + d] = x[e];
                 }
             }
 #pragma unroll
             for (int cp = 0; cp < 2; ++cp) {
                 const uint32_t off = tile_off(32 * th + 16 * cp + 8 * (t >> 4) + (t & 7),
                                               d0 + 16 * hh + (t & 8));
-                const float *v = yi + 8 * cp;
+                const float *u = x + 8 * cp;
                 if (!kF32)
-                    stmatrix_t(orow + off, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    stmatrix_t(orow + off, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                               pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
                 if (kDot) {
                     uint32_t q[4];
                     ldmatrix_t(drow + off, q);
                     float *s = acc + 4 * cp;
-                    s[0] = fmaf(v[0], bf_lo(q[0]), fmaf(v[2], bf_lo(q[1]), s[0]));
-                    s[1] = fmaf(v[1], bf_hi(q[0]), fmaf(v[3], bf_hi(q[1]), s[1]));
-                    s[2] = fmaf(v[4], bf_lo(q[2]), fmaf(v[6], bf_lo(q[3]), s[2]));
-                    s[3] = fmaf(v[5], bf_hi(q[2]), fmaf(v[7], bf_hi(q[3]), s[3]));
+                    s[0] = fmaf(u[0], bf_lo(q[0]), fmaf(u[2], bf_lo(q[1]), s[0]));
+                    s[1] = fmaf(u[1], bf_hi(q[0]), fmaf(u[3], bf_hi(q[1]), s[1]));
+                    s[2] = fmaf(u[4], bf_lo(q[2]), fmaf(u[6], bf_lo(q[3]), s[2]));
+                    s[3] = fmaf(u[5], bf_hi(q[2]), fmaf(u[7], bf_hi(q[3]), s[3]));
                 }
             }
         }
@@ -337,7 +363,7 @@ __global__ void __launch_bounds__(kThr, 1)
 linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant__ TcMaps maps) {
     typedef TcSmem<D, kBwd, kFull> Smem;
     typedef Cols<D, kBwd, kFull> C;
-    constexpr int kStages = Smem::kStages;
+    constexpr int kStages = Smem::kStages, kSlots = Smem::kSlots;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
     Smem &S = *reinterpret_cast<Smem *>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -377,9 +403,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         for (int k = 0; k < kSlots; ++k) mbar_init(&S.factors[k], 1);
         mbar_init(&S.st_full, 8);
         mbar_init(&S.st_empty, 1);
+        mbar_init(&S.drain, 1);
         mbar_init(&S.o_full, 1);
         mbar_init(&S.o_empty, 4);
-        mbar_init(&S.drain, 1);
         mbar_init(&S.o_sync, 4);
         S.abort = 0;
         fence_barrier_init();
@@ -398,11 +424,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         if (lane == 0) mbar_arrive(bar);
     };
     bool ok = true;
-    // Chunk i's factors stand in slot i % kSlots. The producer runs at most
-    // kStages (≤ 6) chunks ahead of the MMAs and every reader of chunk i is done
-    // before the MMAs of chunk i + 2 end, so a slot is free when its turn comes.
-    // Roles that hold no stage wait for the slot's barrier: a stage's could be two
-    // phases on by then.
+    // Chunk i's factors stand in slot i % kSlots. They are written once the MMAs of
+    // chunk i − kStages are done. Full pass: those of chunk i − 3 wait for the outputs
+    // of chunk i − 4, so six slots do; states: those of chunk i − 6 for the state of
+    // chunk i − 8. Roles that hold no stage wait for the slot's barrier: a stage's
+    // could be two phases on by then.
     constexpr int kBufs = (int)C::Bufs;
     if (warp < 4) {
     if (warp == kWarpTma) {
@@ -458,25 +484,29 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (lane >= m) sum += o;
             }
             const double end = __shfl_sync(0xffffffffu, sum, 31);
+            // A: the log2 of what separates a token from the state entering (in the sweep's
+            // direction); a pair's weight is 2^(A_row − A_col)
             const double G[2] = {sum - g1, sum};
-            float up[2], down[2];
+            float A[2], row[2], colf[2], colw[2];
+            bool far = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                up[e] = ex2_approx((float)G[e]);
-                down[e] = ex2_approx((float)(end - G[e]));
+                A[e] = (float)(rev ? end - G[e] : G[e]);
+                far = far || !(fabsf(A[e]) <= kRange);
+                row[e] = a.row_scale * ex2_approx(A[e]);
+                colf[e] = a.col_scale * ex2_approx(-A[e]);
+                colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
             }
+            far = __any_sync(0xffffffffu, far);
             const int sl = i % kSlots;
-            *reinterpret_cast<float2 *>(&S.G[sl][2 * lane]) = make_float2((float)G[0], (float)G[1]);
-            *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) =
-                make_float2(a.row_scale * (rev ? down[0] : up[0]),
-                            a.row_scale * (rev ? down[1] : up[1]));
-            *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) =
-                make_float2(a.col_scale * (rev ? up[0] : down[0]),
-                            a.col_scale * (rev ? up[1] : down[1]));
-            if (lane == 0) S.decay[sl] = ex2_approx((float)end);
-            const bool none = (rev ? down[0] : up[0]) == 0.f || (rev ? down[1] : up[1]) == 0.f;
-            const bool reset = __any_sync(0xffffffffu, none);
-            if (lane == 0) S.reset[sl] = reset;
+            *reinterpret_cast<float2 *>(&S.A[sl][2 * lane]) = make_float2(A[0], A[1]);
+            *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) = make_float2(row[0], row[1]);
+            *reinterpret_cast<float2 *>(&S.colf[sl][2 * lane]) = make_float2(colf[0], colf[1]);
+            *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) = make_float2(colw[0], colw[1]);
+            if (lane == 0) {
+                S.decay[sl] = ex2_approx((float)end);
+                S.strong[sl] = far;
+            }
             seg_log2 += end;
             arrive(&S.full[s]);
             if (lane == 0) mbar_arrive(&S.factors[sl]);
@@ -490,7 +520,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         }
     } else if (warp == kWarpMma) {
         // ---- MMA issuer ---------------------------------------------------------------
-        // The warp waits (a lane per barrier, so that two waits cost one), lane 0 issues.
+        // The warp waits (a lane per barrier, so that two waits cost one), an elected
+        // lane issues. Descriptors are a tile's first plus an offset in 16-byte units:
+        // an MMA of 64 columns is bound by its issue (about 50 clocks).
         constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
         constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
         constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
@@ -503,17 +535,19 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             tc_fence_after();
             return ok;
         };
-        auto kmajor = [&](uint32_t base, int k) {  // K step k of 16 columns
-            return umma_desc_sw128(base + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024);
-        };
+        // K-major: steps of 16 columns inside slabs of 64; M- or N-major: steps of 16
+        // tokens, two 8-row atoms
+        auto kstep = [](int x) { return (uint64_t)(((x >> 2) * kSlab + (x & 3) * 32) >> 4); };
+        constexpr uint64_t kTok = 2048 >> 4;
         auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
             const int s = i % kStages;
+            const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024),
+                           k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), 16, 1024);
             if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
-            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][Smem::kK]);
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_bf16(tmem + C::S, kmajor(q, x), kmajor(k, x), id_s, x > 0);
+                    umma_bf16(tmem + C::S, q + kstep(x), k + kstep(x), id_s, x > 0);
                 umma_commit(&S.s_full);
             }
             __syncwarp();
@@ -521,20 +555,17 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         if (kFull && n > 0) scores(0);
         for (int i = 0; ok && i < n; ++i) {
             const int s = i % kStages;
-            const uint32_t q = smem_addr(S.tile[s][0]), k = smem_addr(S.tile[s][Smem::kK]),
-                           v = smem_addr(S.tile[s][Smem::kV]);
+            const uint64_t k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), kSlab, 1024);
             const int buf = i % kBufs, use = i / kBufs;
-            // U: both operands' K is the token (16 tokens = two 8-row atoms of a slab). Its
-            // tiles have landed: c ◦ V was made from them.
+            // U: both operands' K is the token. Its tiles have landed: c ◦ V was made from them.
             if (!wait2(&S.vp_full[buf], use, &S.u_empty[buf], (use & 1) ^ 1)) break;
-            if (lane == 0) {
+            if (elect_one()) {
+                const uint32_t u = tmem + C::U + buf * D, vp = tmem + C::Vp + buf * C::VpNext;
 #pragma unroll
                 for (int part = 0; part < (int)C::VpParts; ++part)
 #pragma unroll
                     for (int x = 0; x < kC / 16; ++x)
-                        umma_bf16_ts(tmem + C::U + buf * D,
-                                     tmem + C::Vp + buf * C::VpNext + part * 32 + x * 8,
-                                     umma_desc_sw128(k + x * 2048, kSlab, 1024), id_u,
+                        umma_bf16_ts(u, vp + part * 32 + x * 8, k + x * kTok, id_u,
                                      part > 0 || x > 0);
                 umma_commit(&S.u_full[buf]);
                 if (!kFull) umma_commit(&S.empty[s]);
@@ -542,25 +573,29 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             __syncwarp();
             if (!kFull) continue;
             if (i + 1 < n) scores(i + 1);
-            // Ye and Yi
+            // Ye = S_inᵀ Qᵀ and Yi = Vᵀ Pᵀ, the second on top of the first where the row
+            // factors stand in the outputs
+            const bool two = kBwd || S.strong[i % kSlots] != 0;
+            const uint32_t yi = tmem + C::Yi, ye = two ? tmem + C::Ye : yi;
+            const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024);
             if (!ok || !wait2(&S.o_empty, (i & 1) ^ 1, &S.st_full, i)) break;
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (int)C::StParts; ++part)
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x)
-                        umma_bf16_ts(tmem + C::Ye, tmem + C::St + part * (D / 2) + x * 8,
-                                     kmajor(q, x), id_ye, part > 0 || x > 0);
+                        umma_bf16_ts(ye, tmem + C::St + part * (D / 2) + x * 8, q + kstep(x), id_ye,
+                                     part > 0 || x > 0);
                 umma_commit(&S.st_empty);
             }
             __syncwarp();
+            const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
+                           pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
             if (!wait2(&S.p_full, i, &S.p_full, i)) break;
-            if (lane == 0) {
-                const uint32_t pp = smem_addr(S.P);
+            if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < kC / 16; ++x)
-                    umma_bf16(tmem + C::Yi, umma_desc_sw128(v + x * 2048, kSlab, 1024),
-                              umma_desc_sw128(pp + x * 32, 16, 1024), id_yi, x > 0);
+                    umma_bf16(yi, v + x * kTok, pp + kstep(x), id_yi, !two || x > 0);
                 umma_commit(&S.o_full);
                 umma_commit(&S.p_empty);
                 umma_commit(&S.empty[s]);
@@ -569,57 +604,53 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         }
         if (!ok) {  // MMAs in flight end before tensor memory is given back
             const int none = 0;
-            if (lane == 0) {
+            if (elect_one()) {
                 umma_commit(&S.drain);
                 wait_bar(&S.drain, 0, &none);
             }
             __syncwarp();
         }
     } else {
-        // ---- P: weights of the products inside the chunk ------------------------------
+        // ---- P: weights of the products inside the chunk, a row per lane ---------------
         if (kFull) {
             const int r = 32 * warp + lane;
-            // the products' scale goes into the exponent, its sign onto the result
-            const float log_p = lg2_approx(fabsf(a.p_scale));
-            const uint32_t sign_p = a.p_scale < 0.f ? 0x80008000u : 0u;
             for (int i = 0; i < n; ++i) {
-                const int s = i % kStages;
-                const int nq = min(kC, len - chunk_of(i) * kC);
-                ok = wait(&S.full[s], i / kStages) && wait(&S.s_full, i & 1);
+                const int nq = min(kC, len - chunk_of(i) * kC), sl = i % kSlots;
+                ok = wait(&S.factors[sl], i / kSlots) && wait(&S.s_full, i);
                 if (!ok) break;
                 tc_fence_after();
-                const float *G = S.G[i % kSlots];
-                const float gr = G[r] + (rev ? -log_p : log_p);
+                const bool strong = S.strong[sl] != 0;
+                const float rf = S.rowf[sl][r], ar = S.A[sl][r], both = a.row_scale * a.col_scale;
                 const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
                 char *row = reinterpret_cast<char *>(S.P) + r * 128;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t out[16];
-                    if (rev ? half < warp : half > warp) {  // all masked for the warp
+                    if (rev ? half < warp : half > warp) {  // past the diagonal for the warp
 #pragma unroll
                         for (int k = 0; k < 16; ++k) out[k] = 0;
                     } else {
                         float v[32];
                         tmem_ld32(tmem + lanes + C::S + 32 * half, v);
-                        if (rev)
-                            score_weights<true>(v, G + 32 * half, gr, lo - 32 * half,
-                                                hi - 32 * half, out);
+                        if (strong)
+                            score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar,
+                                                      lo - 32 * half, hi - 32 * half, out);
                         else
-                            score_weights<false>(v, G + 32 * half, gr, lo - 32 * half,
-                                                 hi - 32 * half, out);
+                            score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
+                                                       lo - 32 * half, hi - 32 * half, out);
                     }
-                    if (half == 0)
+                    if (half == 0) {
                         ok = wait(&S.p_empty, (i & 1) ^ 1);
-                    else {
+                        if (!ok) break;
+                    } else {
                         tc_fence_before();
                         arrive(&S.s_empty);  // the next chunk's scores may come
                     }
-                    if (!ok) break;
 #pragma unroll
                     for (int c8 = 0; c8 < 4; ++c8)
                         *reinterpret_cast<uint4 *>(row + (((4 * half + c8) ^ (r & 7)) << 4)) =
-                            make_uint4(out[4 * c8] ^ sign_p, out[4 * c8 + 1] ^ sign_p,
-                                       out[4 * c8 + 2] ^ sign_p, out[4 * c8 + 3] ^ sign_p);
+                            make_uint4(out[4 * c8], out[4 * c8 + 1], out[4 * c8 + 2],
+                                       out[4 * c8 + 3]);
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
@@ -652,20 +683,16 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 ok = wait(&S.v_sync[group], syncs++);
                 if (!ok) break;
             }
-            if (use > 0) {
-                ok = wait(&S.u_full[buf], use - 1);  // U has read the previous parts
-                if (!ok) break;
-                tc_fence_after();
-            }
-            if (d0 < D) {
-                const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
-                const float *w = S.colw[i % kSlots];
-                const uint32_t at = tmem + lanes + C::Vp + buf * C::VpNext;
-                // rolled: the loop bodies of the five roles share the instruction caches
+            const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
+            const float *w = S.colw[i % kSlots];
+            const uint32_t at = tmem + lanes + C::Vp + buf * C::VpNext;
+            // rolled: the loop bodies of the five roles share the instruction caches. The
+            // first quarter is made while U still reads the previous parts.
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {  // 32 tokens × 16 columns
-                    const int th = q >> 1, hh = q & 1;
-                    uint32_t part[3][8];
+            for (int q = 0; q < 4; ++q) {  // 32 tokens × 16 columns
+                const int th = q >> 1, hh = q & 1;
+                uint32_t part[3][8];
+                if (d0 < D) {
 #pragma unroll
                     for (int cp = 0; cp < 2; ++cp) {
                         uint32_t v[4];
@@ -690,12 +717,20 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                             }
                         }
                     }
+                }
+                if (q == 0 && use > 0) {
+                    ok = wait(&S.u_full[buf], use - 1);  // U has read the previous parts
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (d0 < D) {
 #pragma unroll
                     for (int e = 0; e < (int)C::VpParts; ++e)
                         tmem_st_frag(at + ((uint32_t)(16 * hh) << 16) + e * 32 + 16 * th, part[e]);
                 }
-                tmem_st_wait();
             }
+            if (!ok) break;
+            if (d0 < D) tmem_st_wait();
             tc_fence_before();
             arrive(&S.vp_full[buf]);
         }
@@ -807,15 +842,22 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                                       ((long long)b * p.seqlen + t0) * y_row + h * a.dv
                                 : nullptr;
                 const bf16 *dot = S.tile[s][Smem::kTiles - 1];
+                const uint32_t t_y = tmem + lanes + C::Yi, t_ye = tmem + lanes + C::Ye;
+                auto done = [&]() {  // the next chunk's products may come
+                    tc_fence_before();
+                    arrive(&S.o_empty);
+                };
                 auto rows = [&](auto is_f32, auto is_dot) {
-                    if (S.reset[i % kSlots])
-                        output_rows<decltype(is_f32)::value, decltype(is_dot)::value, true>(
-                            tmem + lanes + C::Yi, tmem + lanes + C::Ye, S.out, dot,
-                            S.red[warp & 3], S.rowf[i % kSlots], d0, yf, y_row, nl, a.dv);
+                    constexpr bool kF32 = decltype(is_f32)::value, kDot = decltype(is_dot)::value;
+                    const int sl = i % kSlots;
+                    if (S.strong[sl])
+                        output_rows<kF32, kDot, true, true>(t_y, t_ye, S.out, dot, S.red[warp & 3],
+                                                            S.rowf[sl], d0, yf, y_row, nl, a.dv,
+                                                            done);
                     else
-                        output_rows<decltype(is_f32)::value, decltype(is_dot)::value, false>(
-                            tmem + lanes + C::Yi, tmem + lanes + C::Ye, S.out, dot,
-                            S.red[warp & 3], S.rowf[i % kSlots], d0, yf, y_row, nl, a.dv);
+                        output_rows<kF32, kDot, kBwd, false>(t_y, t_ye, S.out, dot,
+                                                             S.red[warp & 3], S.rowf[sl], d0, yf,
+                                                             y_row, nl, a.dv, done);
                 };
                 if constexpr (kBwd) {
                     if (has_dot && f32)
@@ -829,9 +871,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 } else {
                     rows(No(), No());
                 }
+            } else {
+                arrive(&S.o_empty);
             }
-            tc_fence_before();
-            arrive(&S.o_empty);
             if (has_dot) arrive(&S.empty[s]);
             fence_proxy_async_smem();
             arrive(&S.o_sync);
@@ -868,6 +910,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         *reinterpret_cast<volatile int *>(&S.abort) = 1;
         if (p.status) atomicCAS(p.status, 0, kStatusLinattnWait);
     }
+    // The block's barrier takes a warp as arrived once one of its lanes is: a lane that
+    // still issues or stores comes first.
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpTma) tmem_dealloc(tmem, 512);

@@ -205,14 +205,22 @@ __device__ __forceinline__ uint32_t tile_off(int j, int d) {
 
 // ---- sizes -------------------------------------------------------------------------
 // Tensor-memory columns. The pass over the segments' own states holds U and
-// c ◦ V twice instead of the rest.
+// c ◦ V twice instead of the rest. The full forward pass holds c ◦ V twice too: at
+// D = 128 the second copy's first two parts lie where Ye does, which only a strong
+// chunk uses, and the third in the last columns.
 template <int D, bool kBwd, bool kFull> struct Cols {
     static constexpr uint32_t S = 0, Yi = 64, Ye = 128, U = kFull ? 192 : 0;
     static constexpr uint32_t St = 192 + D, StParts = kBwd ? 2 : 1;
     static constexpr uint32_t VpParts = kBwd ? 2 : 3;
     static constexpr uint32_t Vp = kFull ? St + StParts * (D / 2) : 2 * D;
-    static constexpr uint32_t VpNext = VpParts * 32, Bufs = kFull ? 1 : 2;
-    static_assert(Vp + Bufs * VpNext <= 512, "tensor memory");
+    static constexpr int UBufs = kFull ? 1 : 2, VpBufs = kFull && kBwd ? 1 : 2;
+    static constexpr bool VpOnYe = kFull && !kBwd && D == 128;
+    static constexpr uint32_t VpNext = VpParts * 32;
+    static __device__ __forceinline__ uint32_t vp(int buf, int part) {
+        if (VpOnYe && buf) return part < 2 ? Ye + 32 * part : Vp + VpNext;
+        return Vp + buf * VpNext + part * 32;
+    }
+    static_assert(Vp + (VpOnYe ? VpNext + 32 : VpBufs * VpNext) <= 512, "tensor memory");
 };
 
 template <int D, bool kBwd, bool kFull> struct TcSmem {
@@ -229,7 +237,7 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     int strong[kSlots];             // the factors of P leave float32's comfortable range
     float red[4][kC];
     uint64_t full[kStages], empty[kStages], factors[kSlots];
-    uint64_t vp_full[2], u_full[2], u_empty[2];
+    uint64_t vp_full[2], vp_empty[2], u_full[2], u_empty[2];
     uint64_t s_full, s_empty, p_full, p_empty, st_full, st_empty;
     uint64_t o_full, o_empty, drain;
     uint64_t v_sync[2], o_sync;     // the warps of c ◦ V, the output warps
@@ -396,6 +404,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         mbar_init(&S.p_empty, 1);
         for (int k = 0; k < 2; ++k) {
             mbar_init(&S.vp_full[k], 4);
+            mbar_init(&S.vp_empty[k], 1);
             mbar_init(&S.u_full[k], 1);
             mbar_init(&S.u_empty[k], 8);
             mbar_init(&S.v_sync[k], 4);
@@ -429,7 +438,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     // of chunk i − 4, so six slots do; states: those of chunk i − 6 for the state of
     // chunk i − 8. Roles that hold no stage wait for the slot's barrier: a stage's
     // could be two phases on by then.
-    constexpr int kBufs = (int)C::Bufs;
+    constexpr int kUBufs = C::UBufs, kVBufs = C::VpBufs;
     if (warp < 4) {
     if (warp == kWarpTma) {
         // ---- producer: tiles by TMA, decays by the warp -----------------------------
@@ -520,7 +529,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         }
     } else if (warp == kWarpMma) {
         // ---- MMA issuer ---------------------------------------------------------------
-        // The warp waits (a lane per barrier, so that two waits cost one), an elected
+        // The warp waits (a lane per barrier, so that several waits cost one), an elected
         // lane issues. Descriptors are a tile's first plus an offset in 16-byte units:
         // an MMA of 64 columns is bound by its issue (about 50 clocks).
         constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
@@ -528,12 +537,18 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
         constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
         constexpr uint32_t kSlab = kC * 128;
-        auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) -> bool {
+        auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2,
+                         uint32_t p2) -> bool {
             bool done = true;
-            if (lane < 2) done = wait_bar(lane ? b1 : b0, (lane ? p1 : p0) & 1, &S.abort);
+            if (lane < 3)
+                done = wait_bar(lane == 0 ? b0 : lane == 1 ? b1 : b2,
+                                (lane == 0 ? p0 : lane == 1 ? p1 : p2) & 1, &S.abort);
             ok = __all_sync(0xffffffffu, done);
             tc_fence_after();
             return ok;
+        };
+        auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) -> bool {
+            return wait3(b0, p0, b1, p1, b1, p1);
         };
         // K-major: steps of 16 columns inside slabs of 64; M- or N-major: steps of 16
         // tokens, two 8-row atoms
@@ -556,18 +571,19 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         for (int i = 0; ok && i < n; ++i) {
             const int s = i % kStages;
             const uint64_t k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), kSlab, 1024);
-            const int buf = i % kBufs, use = i / kBufs;
+            const int ub = i % kUBufs, vb = i % kVBufs;
             // U: both operands' K is the token. Its tiles have landed: c ◦ V was made from them.
-            if (!wait2(&S.vp_full[buf], use, &S.u_empty[buf], (use & 1) ^ 1)) break;
+            if (!wait2(&S.vp_full[vb], i / kVBufs, &S.u_empty[ub], ((i / kUBufs) & 1) ^ 1)) break;
             if (elect_one()) {
-                const uint32_t u = tmem + C::U + buf * D, vp = tmem + C::Vp + buf * C::VpNext;
+                const uint32_t u = tmem + C::U + ub * D;
 #pragma unroll
                 for (int part = 0; part < (int)C::VpParts; ++part)
 #pragma unroll
                     for (int x = 0; x < kC / 16; ++x)
-                        umma_bf16_ts(u, vp + part * 32 + x * 8, k + x * kTok, id_u,
+                        umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok, id_u,
                                      part > 0 || x > 0);
-                umma_commit(&S.u_full[buf]);
+                umma_commit(&S.u_full[ub]);
+                if (kVBufs != kUBufs) umma_commit(&S.vp_empty[vb]);
                 if (!kFull) umma_commit(&S.empty[s]);
             }
             __syncwarp();
@@ -578,7 +594,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             const bool two = kBwd || S.strong[i % kSlots] != 0;
             const uint32_t yi = tmem + C::Yi, ye = two ? tmem + C::Ye : yi;
             const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024);
-            if (!ok || !wait2(&S.o_empty, (i & 1) ^ 1, &S.st_full, i)) break;
+            const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
+                           pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
+            if (!ok || !wait3(&S.o_empty, (i & 1) ^ 1, &S.st_full, i, &S.p_full, i)) break;
             if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (int)C::StParts; ++part)
@@ -587,12 +605,6 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                         umma_bf16_ts(ye, tmem + C::St + part * (D / 2) + x * 8, q + kstep(x), id_ye,
                                      part > 0 || x > 0);
                 umma_commit(&S.st_empty);
-            }
-            __syncwarp();
-            const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
-                           pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
-            if (!wait2(&S.p_full, i, &S.p_full, i)) break;
-            if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < kC / 16; ++x)
                     umma_bf16(yi, v + x * kTok, pp + kstep(x), id_yi, !two || x > 0);
@@ -623,28 +635,36 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 const float rf = S.rowf[sl][r], ar = S.A[sl][r], both = a.row_scale * a.col_scale;
                 const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
                 char *row = reinterpret_cast<char *>(S.P) + r * 128;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t out[16];
-                    if (rev ? half < warp : half > warp) {  // past the diagonal for the warp
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) out[k] = 0;
-                    } else {
-                        float v[32];
-                        tmem_ld32(tmem + lanes + C::S + 32 * half, v);
-                        if (strong)
-                            score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar,
-                                                      lo - 32 * half, hi - 32 * half, out);
-                        else
-                            score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
-                                                       lo - 32 * half, hi - 32 * half, out);
-                    }
-                    if (half == 0) {
-                        ok = wait(&S.p_empty, (i & 1) ^ 1);
-                        if (!ok) break;
-                    } else {
+                uint32_t out[16];
+                auto block = [&](int half, bool last) {
+                    float v[32];
+                    tmem_ld32(tmem + lanes + C::S + 32 * half, v);
+                    if (last) {
                         tc_fence_before();
                         arrive(&S.s_empty);  // the next chunk's scores may come
+                    }
+                    if (strong)
+                        score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar, lo - 32 * half,
+                                                  hi - 32 * half, out);
+                    else
+                        score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
+                                                   lo - 32 * half, hi - 32 * half, out);
+                };
+                // the block off the diagonal (of the warp that has one, else zeros), then
+                // the one on it
+                const bool off = warp == (rev ? 0 : 1);
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    const int half = k ? warp : 1 - warp;
+                    if (k || off) {
+                        block(half, k == 1);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) out[e] = 0;
+                    }
+                    if (k == 0) {
+                        ok = wait(&S.p_empty, (i & 1) ^ 1);
+                        if (!ok) break;
                     }
 #pragma unroll
                     for (int c8 = 0; c8 < 4; ++c8)
@@ -664,8 +684,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         const int group = warp >= 16 ? 1 : 0, tg = t - (group ? 512 : 128);
         const int d0 = 32 * (warp & 3), r8 = lane >> 4, c2 = 2 * (lane & 3);
         uint32_t syncs = 0;
-        for (int i = group; i < n; i += kBufs) {
-            const int s = i % kStages, buf = i % kBufs, use = i / kBufs;
+        for (int i = group; i < n; i += kFull ? 1 : 2) {
+            const int s = i % kStages, vb = i % kVBufs, use = i / kVBufs;
             const int nq = min(kC, len - chunk_of(i) * kC);
             ok = wait(&S.full[s], i / kStages);
             if (!ok) break;
@@ -685,7 +705,6 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             }
             const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
             const float *w = S.colw[i % kSlots];
-            const uint32_t at = tmem + lanes + C::Vp + buf * C::VpNext;
             // rolled: the loop bodies of the five roles share the instruction caches. The
             // first quarter is made while U still reads the previous parts.
 #pragma unroll 1
@@ -718,21 +737,30 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                         }
                     }
                 }
+                if (C::VpOnYe && q == 0 && vb && i > 0 &&
+                    (S.strong[(i - 1) % kSlots] || (i > 1 && S.strong[(i - 2) % kSlots]))) {
+                    ok = wait(&S.o_empty, i - 1);  // a strong chunk's Ye has been read
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (q == 0 && use > 0) {
-                    ok = wait(&S.u_full[buf], use - 1);  // U has read the previous parts
+                    // U has read what stands there
+                    ok = wait(kVBufs == kUBufs ? &S.u_full[vb] : &S.vp_empty[vb], use - 1);
                     if (!ok) break;
                     tc_fence_after();
                 }
                 if (d0 < D) {
 #pragma unroll
                     for (int e = 0; e < (int)C::VpParts; ++e)
-                        tmem_st_frag(at + ((uint32_t)(16 * hh) << 16) + e * 32 + 16 * th, part[e]);
+                        tmem_st_frag(tmem + lanes + ((uint32_t)(16 * hh) << 16) + C::vp(vb, e) +
+                                         16 * th,
+                                     part[e]);
                 }
             }
             if (!ok) break;
             if (d0 < D) tmem_st_wait();
             tc_fence_before();
-            arrive(&S.vp_full[buf]);
+            arrive(&S.vp_full[vb]);
         }
     } else if (warp < 16) {
         // ---- state: lane d, columns half·D/2 .. ------------------------------------------
@@ -755,7 +783,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             for (int k = 0; k < kH; ++k) st[k] = k < cols ? src[k * step] : 0.f;
         }
         for (int i = 0; i < n; ++i) {
-            const int buf = i % kBufs, use = i / kBufs;
+            const int buf = i % kUBufs, use = i / kUBufs;
             if (kFull) {
                 ok = wait(&S.st_empty, (i & 1) ^ 1);
                 if (!ok) break;

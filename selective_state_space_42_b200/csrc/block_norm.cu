@@ -22,12 +22,17 @@
 namespace selscan {
 namespace {
 
-// kVec consecutive elements as floats (plain loads: `out` may be `res`).
-template <typename T, int kVec> struct Io;
-template <> struct Io<float, 8> {
-    static __device__ __forceinline__ void ld(const void *p, long long i, float (&v)[8]) {
+// kVec consecutive elements of a row, as they stand in memory until they are
+// used (a bfloat16 vector takes half the registers of its floats).
+template <typename T, int kVec> struct Raw;
+template <> struct Raw<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void ld(const void *p, long long i) {
         const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 a = q[0], b = q[1];
+        a = q[0];
+        b = q[1];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
@@ -37,10 +42,12 @@ template <> struct Io<float, 8> {
         q[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
-template <> struct Io<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void ld(const void *p, long long i, float (&v)[8]) {
-        const uint4 u =
-            *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+template <> struct Raw<__nv_bfloat16, 8> {
+    uint4 u;
+    __device__ __forceinline__ void ld(const void *p, long long i) {
+        u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -59,123 +66,140 @@ template <> struct Io<__nv_bfloat16, 8> {
             make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
-template <typename T> struct Io<T, 1> {
-    static __device__ __forceinline__ void ld(const void *p, long long i, float (&v)[1]) {
-        v[0] = to_f32(static_cast<const T *>(p)[i]);
+template <typename T> struct Raw<T, 1> {
+    T u;
+    __device__ __forceinline__ void ld(const void *p, long long i) {
+        u = static_cast<const T *>(p)[i];
     }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f32(u); }
     static __device__ __forceinline__ void st(void *p, long long i, const float (&v)[1]) {
         static_cast<T *>(p)[i] = from_f32<T>(v[0]);
     }
 };
+template <int kVec> __device__ __forceinline__ void ld_weight(const float *p, int c, float (&v)[kVec]) {
+    Raw<float, kVec> r;
+    r.ld(p, c);
+    r.get(v);
+}
 
-// Where a thread's columns are. tg threads a group, groups·tg threads a row,
-// rows_per rows a block.
+// Where a thread's columns are: tg threads a group, row_threads a row, rows_per
+// rows a block.
 struct Map {
     int tg, row_threads, rows_per;
 };
 
-// Sum over the tg threads of this thread's group (a power of two up to a
-// warp, or whole warps); `red` has a float per warp. Every thread of the
-// block calls it.
-__device__ __forceinline__ float group_sum(float v, int tg, float *red) {
-    const int w = threadIdx.x >> 5;
-    if (tg <= 32) {
-        for (int m = tg >> 1; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+// Sums of a float2 over the threads of this thread's group or row: `threads` is
+// a power of two up to a warp, or whole warps starting at a multiple of it (the
+// whole block for a row). Every thread of the block calls it; `red` has a float2
+// per warp, and another call's until two block barriers later.
+__device__ __forceinline__ float2 sum_over(float2 v, int threads, float2 *red) {
+    if (threads <= 32) {
+        for (int m = threads >> 1; m > 0; m >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
+        }
         return v;
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    __syncthreads();  // readers of the previous sum are done
+    for (int m = 16; m > 0; m >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
+    }
+    const int w = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) red[w] = v;
     __syncthreads();
-    const int per = tg >> 5, first = w / per * per;
-    float s = 0.f;
-    for (int k = 0; k < per; ++k) s += red[first + k];
-    return s;
-}
-
-// Sums over a row's threads. Rows of more than a warp have the block to
-// themselves; a row of fewer threads than a warp has a power of two.
-__device__ __forceinline__ float row_sum(float v, int row_threads, float *red) {
-    if (row_threads <= 32) {
-        for (int m = row_threads >> 1; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        return v;
+    const int per = threads >> 5, first = w / per * per;
+    float2 s = make_float2(0.f, 0.f);
+    for (int k = 0; k < per; ++k) {
+        const float2 r = red[first + k];
+        s.x += r.x;
+        s.y += r.y;
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-    const int nw = ((int)blockDim.x + 31) >> 5;
-    for (int k = 0; k < nw; ++k) s += red[k];
     return s;
 }
 
-template <typename T, typename TR, int kVec, int kNV>
-__global__ void __launch_bounds__(1024) block_norm_fwd_kernel(const BlockNormParams p, const Map m) {
-    __shared__ float red[32];
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
+    __shared__ float2 red[2][32];
     const int t = threadIdx.x, local = t % m.row_threads;
     const long long row = (long long)blockIdx.x * m.rows_per + t / m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
     const bool live = row < p.rows && grp < p.groups;
-    float v[kNV][kVec], gate[kNV][kVec], res[kNV][kVec];
+    Raw<T, kVec> x[kNV], z[kNV];
+    Raw<TR, kVec> res[kNV];
+    float v[kNV][kVec];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
         if (!live || e >= gs) continue;
         const long long c = (long long)grp * gs + e;
-        Io<T, kVec>::ld(p.x, row * p.x_row + c, v[i]);
-        if (p.gate != kGateNone) Io<T, kVec>::ld(p.z, row * p.z_row + c, gate[i]);
-        if (p.res) Io<TR, kVec>::ld(p.res, row * p.dim + c, res[i]);
+        x[i].ld(p.x, row * p.x_row + c);
+        if (p.gate != kGateNone) z[i].ld(p.z, row * p.z_row + c);
+        if (p.res) res[i].ld(p.res, row * p.dim + c);
     }
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
         if (!live || e >= gs) continue;
+        x[i].get(v[i]);
+        if (p.gate == kGateBefore) {
+            float g[kVec];
+            z[i].get(g);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            if (p.gate != kGateNone) gate[i][k] = silu_f32(gate[i][k]);
-            if (p.gate == kGateBefore) v[i][k] *= gate[i][k];
-            sum = fmaf(v[i][k], v[i][k], sum);
+            for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(g[k]);
         }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum = fmaf(v[i][k], v[i][k], sum);
     }
     float rstd = 1.f;
-    if (p.weight) rstd = rsqrtf(group_sum(sum, m.tg, red) / (float)gs + p.eps);
+    if (p.weight)
+        rstd = rsqrtf(sum_over(make_float2(sum, 0.f), m.tg, red[0]).x / (float)gs + p.eps);
     float sum2 = 0.f;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
         if (!live || e >= gs) continue;
         const int c = grp * gs + e;
-        float w[kVec], s[kVec];
-        if (p.weight) Io<float, kVec>::ld(p.weight, c, w);
-        if (p.res_scale) Io<float, kVec>::ld(p.res_scale, c, s);
+        float f[kVec];
+        if (p.weight) {
+            ld_weight<kVec>(p.weight, c, f);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            float u = v[i][k];
-            if (p.weight) u = u * rstd * w[k];
-            if (p.gate == kGateAfter) u *= gate[i][k];
-            if (p.res_scale) u *= s[k];
-            if (p.res) u += res[i][k];
-            v[i][k] = u;
-            sum2 = fmaf(u, u, sum2);
+            for (int k = 0; k < kVec; ++k) v[i][k] *= rstd * f[k];
         }
-        if (p.out) Io<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
+        if (p.gate == kGateAfter) {
+            z[i].get(f);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(f[k]);
+        }
+        if (p.res_scale) {
+            ld_weight<kVec>(p.res_scale, c, f);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[i][k] *= f[k];
+        }
+        if (p.res) {
+            res[i].get(f);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[i][k] += f[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum2 = fmaf(v[i][k], v[i][k], sum2);
+        if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
     }
     if (!p.next_weight) return;
-    const float rstd2 = rsqrtf(row_sum(sum2, m.row_threads, red) / (float)p.dim + p.eps);
+    const float rstd2 =
+        rsqrtf(sum_over(make_float2(sum2, 0.f), m.row_threads, red[1]).x / (float)p.dim + p.eps);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
         if (!live || e >= gs) continue;
         const int c = grp * gs + e;
         float w[kVec];
-        Io<float, kVec>::ld(p.next_weight, c, w);
+        ld_weight<kVec>(p.next_weight, c, w);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[i][k] = v[i][k] * rstd2 * w[k];
-        Io<T, kVec>::st(p.y, row * p.dim + c, v[i]);
+        for (int k = 0; k < kVec; ++k) v[i][k] *= rstd2 * w[k];
+        Raw<T, kVec>::st(p.y, row * p.dim + c, v[i]);
     }
 }
 
@@ -189,12 +213,15 @@ __global__ void __launch_bounds__(1024) block_norm_fwd_kernel(const BlockNormPar
 // Everything of the forward is recomputed from the inputs. Blocks stride over
 // the rows and keep the three column sums of their rows in registers; a
 // second kernel adds the blocks' sums in a fixed order.
-template <typename T, typename TR, int kVec, int kNV, int kThreads>
-__global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const BlockNormParams p, const Map m) {
-    __shared__ float red[32];
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
+    __shared__ float2 red[3][32];
+    extern __shared__ float sums[];  // [3][dim] where a block has several rows
     const int t = threadIdx.x, local = t % m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
     const int sub = t / m.row_threads;
+    const bool before = p.gate == kGateBefore, after = p.gate == kGateAfter;
     float aw[kNV][kVec], as[kNV][kVec], an[kNV][kVec];
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
@@ -205,173 +232,234 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const BlockNor
          base += (long long)gridDim.x * m.rows_per) {
         const long long row = base + sub;
         const bool live = row < p.rows && grp < p.groups;
-        float x[kNV][kVec], z[kNV][kVec], r[kNV][kVec], dr[kNV][kVec], dm[kNV][kVec];
+        Raw<T, kVec> xr[kNV], zr[kNV], yr[kNV];
+        Raw<TR, kVec> rr[kNV], dr[kNV];
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int e = (i * m.tg + lane) * kVec;
+            if (!live || e >= gs) continue;
+            const long long c = (long long)grp * gs + e;
+            xr[i].ld(p.x, row * p.x_row + c);
+            if (p.gate != kGateNone) zr[i].ld(p.z, row * p.z_row + c);
+            if (p.res && p.next_weight) rr[i].ld(p.res, row * p.dim + c);
+            if (p.next_weight) yr[i].ld(p.dy, row * p.dim + c);
+            if (p.dout) dr[i].ld(p.dout, row * p.dim + c);
+        }
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
-            if (!live || e >= gs) continue;
-            const long long c = (long long)grp * gs + e;
-            Io<T, kVec>::ld(p.x, row * p.x_row + c, x[i]);
-            if (p.gate != kGateNone) Io<T, kVec>::ld(p.z, row * p.z_row + c, z[i]);
-            if (p.res) Io<TR, kVec>::ld(p.res, row * p.dim + c, r[i]);
-            if (p.dout) Io<TR, kVec>::ld(p.dout, row * p.dim + c, dr[i]);
-            if (p.next_weight) Io<T, kVec>::ld(p.dy, row * p.dim + c, dm[i]);
-        }
+            if (!live || e >= gs || !p.weight) continue;
+            float x[kVec], z[kVec];
+            xr[i].get(x);
+            if (before) {
+                zr[i].get(z);
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int e = (i * m.tg + lane) * kVec;
-            if (!live || e >= gs) continue;
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                float a = x[i][k];
-                if (p.gate == kGateBefore) a *= silu_f32(z[i][k]);
-                sum = fmaf(a, a, sum);
+                for (int k = 0; k < kVec; ++k) x[k] *= silu_f32(z[k]);
             }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum = fmaf(x[k], x[k], sum);
         }
         float rstd = 1.f;
-        if (p.weight) rstd = rsqrtf(group_sum(sum, m.tg, red) / (float)gs + p.eps);
+        if (p.weight)
+            rstd = rsqrtf(sum_over(make_float2(sum, 0.f), m.tg, red[0]).x / (float)gs + p.eps);
         // out, its norm's statistics
-        float s_rr = 0.f, s_dr = 0.f;
+        float r[kNV][kVec];
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
-            if (!live || e >= gs) continue;
+            if (!live || e >= gs || !p.next_weight) continue;
             const int c = grp * gs + e;
-            float w[kVec], s[kVec], w2[kVec];
-            if (p.weight) Io<float, kVec>::ld(p.weight, c, w);
-            if (p.res_scale) Io<float, kVec>::ld(p.res_scale, c, s);
-            if (p.next_weight) Io<float, kVec>::ld(p.next_weight, c, w2);
+            float f[kVec];
+            xr[i].get(r[i]);
+            if (p.gate != kGateNone) {
+                zr[i].get(f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) r[i][k] *= silu_f32(f[k]);
+            }
+            if (p.weight) {
+                ld_weight<kVec>(p.weight, c, f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) r[i][k] *= rstd * f[k];
+            }
+            if (p.res_scale) {
+                ld_weight<kVec>(p.res_scale, c, f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) r[i][k] *= f[k];
+            }
+            if (p.res) {
+                rr[i].get(f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) r[i][k] += f[k];
+            }
+            float dy[kVec];
+            yr[i].get(dy);
+            ld_weight<kVec>(p.next_weight, c, f);
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                if (!p.dout) dr[i][k] = 0.f;
-                if (!p.next_weight) continue;
-                float u = x[i][k];
-                if (p.gate == kGateBefore) u *= silu_f32(z[i][k]);
-                if (p.weight) u *= rstd * w[k];
-                if (p.gate == kGateAfter) u *= silu_f32(z[i][k]);
-                if (p.res_scale) u *= s[k];
-                if (p.res) u += r[i][k];
-                r[i][k] = u;
-                s_rr = fmaf(u, u, s_rr);
-                s_dr = fmaf(dm[i][k] * w2[k], u, s_dr);
+                s2.x = fmaf(r[i][k], r[i][k], s2.x);
+                s2.y = fmaf(dy[k] * f[k], r[i][k], s2.y);
             }
         }
         float rstd2 = 1.f, coef = 0.f;
         if (p.next_weight) {
-            rstd2 = rsqrtf(row_sum(s_rr, m.row_threads, red) / (float)p.dim + p.eps);
-            coef = row_sum(s_dr, m.row_threads, red) * rstd2 / (float)p.dim;
+            s2 = sum_over(s2, m.row_threads, red[1]);
+            rstd2 = rsqrtf(s2.x / (float)p.dim + p.eps);
+            coef = s2.y * rstd2 / (float)p.dim;
         }
         float s_dn = 0.f;
+        float d[kNV][kVec];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
             if (!live || e >= gs) continue;
             const int c = grp * gs + e;
-            float w[kVec], s[kVec], w2[kVec];
-            if (p.weight) Io<float, kVec>::ld(p.weight, c, w);
-            if (p.res_scale) Io<float, kVec>::ld(p.res_scale, c, s);
-            if (p.next_weight) Io<float, kVec>::ld(p.next_weight, c, w2);
+            float f[kVec];
+            if (p.dout) {
+                dr[i].get(d[i]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                if (p.next_weight) {
+                for (int k = 0; k < kVec; ++k) d[i][k] = 0.f;
+            }
+            if (p.next_weight) {
+                float dy[kVec];
+                yr[i].get(dy);
+                ld_weight<kVec>(p.next_weight, c, f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
                     const float mm = r[i][k] * rstd2;
-                    an[i][k] = fmaf(dm[i][k], mm, an[i][k]);
-                    dr[i][k] += rstd2 * (dm[i][k] * w2[k] - mm * coef);
+                    an[i][k] = fmaf(dy[k], mm, an[i][k]);
+                    d[i][k] += rstd2 * (dy[k] * f[k] - mm * coef);
                 }
             }
-            if (p.dres) Io<TR, kVec>::st(p.dres, row * p.dim + c, dr[i]);
+            if (p.dres) Raw<TR, kVec>::st(p.dres, row * p.dim + c, d[i]);
+            float n[kVec], z[kVec], w[kVec];
+            xr[i].get(n);
+            if (p.gate != kGateNone) zr[i].get(z);
+            if (before) {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                const float gate = p.gate != kGateNone ? silu_f32(z[i][k]) : 1.f;
-                float a = x[i][k];
-                if (p.gate == kGateBefore) a *= gate;
-                const float n = a * rstd;
-                const float pp = p.weight ? n * w[k] : a;
-                float d = dr[i][k];
-                if (p.res_scale) {
-                    as[i][k] = fmaf(d, p.gate == kGateAfter ? pp * gate : pp, as[i][k]);
-                    d *= s[k];
+                for (int k = 0; k < kVec; ++k) n[k] *= silu_f32(z[k]);
+            }
+            if (p.weight) {
+                ld_weight<kVec>(p.weight, c, w);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) n[k] *= rstd;
+            }
+            if (p.res_scale) {
+                ld_weight<kVec>(p.res_scale, c, f);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    float u = p.weight ? n[k] * w[k] : n[k];
+                    if (after) u *= silu_f32(z[k]);
+                    as[i][k] = fmaf(d[i][k], u, as[i][k]);
+                    d[i][k] *= f[k];
                 }
-                float dg = 0.f;
-                if (p.gate == kGateAfter) {
-                    dg = d * pp;
-                    d *= gate;
+            }
+            if (after) {
+                float dz[kVec];
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    const float sig = sigmoid_f32(z[k]);
+                    const float pp = p.weight ? n[k] * w[k] : n[k];
+                    dz[k] = d[i][k] * pp * sig * (1.f + z[k] * (1.f - sig));
+                    d[i][k] *= z[k] * sig;
                 }
-                if (p.weight) {
-                    aw[i][k] = fmaf(d, n, aw[i][k]);
-                    d *= w[k];
-                    s_dn = fmaf(d, n, s_dn);
+                Raw<T, kVec>::st(p.dz, row * p.dim + c, dz);
+            }
+            if (p.weight) {
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    aw[i][k] = fmaf(d[i][k], n[k], aw[i][k]);
+                    d[i][k] *= w[k];
+                    s_dn = fmaf(d[i][k], n[k], s_dn);
                 }
-                dr[i][k] = d;   // dn (or da where there is no norm)
-                dm[i][k] = dg;  // dgate of a gate after
             }
         }
         float cg = 0.f;
-        if (p.weight) cg = group_sum(s_dn, m.tg, red) / (float)gs;
+        if (p.weight) cg = sum_over(make_float2(s_dn, 0.f), m.tg, red[2]).x / (float)gs;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
             if (!live || e >= gs) continue;
             const long long c = (long long)grp * gs + e;
+            float x[kVec], z[kVec];
+            xr[i].get(x);
+            if (before) zr[i].get(z);
+            float dz[kVec];
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                float a = x[i][k], sig = 0.f, gate = 1.f;
-                if (p.gate != kGateNone) {
-                    sig = sigmoid_f32(z[i][k]);
-                    gate = z[i][k] * sig;
+                float a = x[k], sig = 0.f;
+                if (before) {
+                    sig = sigmoid_f32(z[k]);
+                    a *= z[k] * sig;
                 }
-                if (p.gate == kGateBefore) a *= gate;
-                float d = dr[i][k];
-                if (p.weight) d = rstd * (d - a * rstd * cg);
-                float dg = dm[i][k];
-                if (p.gate == kGateBefore) {
-                    dg = d * x[i][k];
-                    d *= gate;
+                if (p.weight) d[i][k] = rstd * (d[i][k] - a * rstd * cg);
+                if (before) {
+                    dz[k] = d[i][k] * x[k] * sig * (1.f + z[k] * (1.f - sig));
+                    d[i][k] *= z[k] * sig;
                 }
-                dr[i][k] = d;
-                if (p.gate != kGateNone) dm[i][k] = dg * sig * (1.f + z[i][k] * (1.f - sig));
             }
-            Io<T, kVec>::st(p.dx, row * p.dim + c, dr[i]);
-            if (p.gate != kGateNone) Io<T, kVec>::st(p.dz, row * p.dim + c, dm[i]);
+            if (before) Raw<T, kVec>::st(p.dz, row * p.dim + c, dz);
+            Raw<T, kVec>::st(p.dx, row * p.dim + c, d[i]);
         }
     }
-    // the block's column sums, of each of its row slots
-    float *part = p.partial + ((long long)blockIdx.x * m.rows_per + sub) * 3 * p.dim;
+    // the block's column sums; its row slots add theirs in turn
+    float *part = p.partial + (long long)blockIdx.x * 3 * p.dim;
+    if (m.rows_per > 1) {
+        for (int s = 0; s < m.rows_per; ++s) {
+            if (sub == s && grp < p.groups) {
+#pragma unroll
+                for (int i = 0; i < kNV; ++i) {
+                    const int e = (i * m.tg + lane) * kVec;
+                    if (e >= gs) continue;
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) {
+                        const int c = grp * gs + e + k;
+                        sums[c] = (s ? sums[c] : 0.f) + aw[i][k];
+                        sums[p.dim + c] = (s ? sums[p.dim + c] : 0.f) + as[i][k];
+                        sums[2 * p.dim + c] = (s ? sums[2 * p.dim + c] : 0.f) + an[i][k];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        for (int c = t; c < 3 * p.dim; c += blockDim.x) part[c] = sums[c];
+        return;
+    }
     if (grp < p.groups) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
             if (e >= gs) continue;
             const int c = grp * gs + e;
-            if (p.weight) Io<float, kVec>::st(part, c, aw[i]);
-            if (p.res_scale) Io<float, kVec>::st(part + p.dim, c, as[i]);
-            if (p.next_weight) Io<float, kVec>::st(part + 2 * p.dim, c, an[i]);
+            if (p.weight) Raw<float, kVec>::st(part, c, aw[i]);
+            if (p.res_scale) Raw<float, kVec>::st(part + p.dim, c, as[i]);
+            if (p.next_weight) Raw<float, kVec>::st(part + 2 * p.dim, c, an[i]);
         }
     }
 }
 
-// Column sums over the partials' `n` row slots: 32 columns a block, 8 slices
-// of slots.
-__global__ void __launch_bounds__(256)
+// Column sums over the n blocks' partials: 32 columns a block, 32 slices.
+__global__ void __launch_bounds__(1024)
 block_norm_reduce_kernel(const float *__restrict__ partial, int n, int dim, float *dweight,
                          float *dres_scale, float *dnext_weight) {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
     float *out = which == 0 ? dweight : which == 1 ? dres_scale : dnext_weight;
     if (!out) return;
     float v = 0.f;
-    if (c < dim)
-        for (int k = w; k < n; k += 8) v += partial[((long long)k * 3 + which) * dim + c];
+    if (c < dim) {
+#pragma unroll 8
+        for (int k = w; k < n; k += 32) v += partial[((long long)k * 3 + which) * dim + c];
+    }
     s[w][lane] = v;
     __syncthreads();
-    if (w == 0 && c < dim) {
-        float sum = 0.f;
+    float u = s[lane][w];  // column w of the 32, slice `lane`
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += s[k][lane];
-        out[c] = sum;
-    }
+    for (int m = 16; m > 0; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
+    if (lane == 0 && blockIdx.x * 32 + w < dim) out[blockIdx.x * 32 + w] = u;
 }
 
 int pow2_floor(int v) {
@@ -412,10 +500,10 @@ bool fits(const BlockNormParams &p, int vec, int nv, int threads, Map *m) {
 
 bool use_vec(const BlockNormParams &p) { return p.vec && (p.dim / p.groups) % 8 == 0; }
 
-template <typename T, typename TR, int kVec, int kNV>
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
 cudaError_t fwd(const BlockNormParams &p, const Map &m, cudaStream_t stream) {
     const long long blocks = (p.rows + m.rows_per - 1) / m.rows_per;
-    block_norm_fwd_kernel<T, TR, kVec, kNV>
+    block_norm_fwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks>
         <<<(unsigned)blocks, m.row_threads * m.rows_per, 0, stream>>>(p, m);
     return cudaGetLastError();
 }
@@ -424,26 +512,27 @@ template <typename T, typename TR>
 cudaError_t fwd_typed(const BlockNormParams &p, cudaStream_t stream) {
     Map m;
     if (use_vec(p)) {
-        if (fits(p, 8, 1, 1024, &m)) return fwd<T, TR, 8, 1>(p, m, stream);
-        if (fits(p, 8, 2, 1024, &m)) return fwd<T, TR, 8, 2>(p, m, stream);
-        if (fits(p, 8, 4, 1024, &m)) return fwd<T, TR, 8, 4>(p, m, stream);
+        if (fits(p, 8, 1, 640, &m)) return fwd<T, TR, 8, 1, 640, 2>(p, m, stream);
+        if (fits(p, 8, 2, 640, &m)) return fwd<T, TR, 8, 2, 640, 1>(p, m, stream);
+        if (fits(p, 8, 4, 512, &m)) return fwd<T, TR, 8, 4, 512, 1>(p, m, stream);
     }
-    if (fits(p, 1, 8, 1024, &m)) return fwd<T, TR, 1, 8>(p, m, stream);
-    if (fits(p, 1, 32, 1024, &m)) return fwd<T, TR, 1, 32>(p, m, stream);
+    if (fits(p, 1, 8, 512, &m)) return fwd<T, TR, 1, 8, 512, 2>(p, m, stream);
+    if (fits(p, 1, 32, 1024, &m)) return fwd<T, TR, 1, 32, 1024, 1>(p, m, stream);
     return cudaErrorInvalidValue;
 }
 
-template <typename T, typename TR, int kVec, int kNV, int kThreads>
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
 cudaError_t bwd(const BlockNormParams &p, const Map &m, cudaStream_t stream) {
     const long long want = (p.rows + m.rows_per - 1) / m.rows_per;
-    const int blocks =
-        (int)std::min<long long>(want, block_norm_bwd_slots(p.rows, p.dim) / m.rows_per);
-    block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads>
-        <<<blocks, m.row_threads * m.rows_per, 0, stream>>>(p, m);
+    const int threads = m.row_threads * m.rows_per;
+    const int blocks = (int)std::min<long long>(want, block_norm_bwd_blocks(p.rows, p.dim, std::max(threads, 128)));
+    const int smem = m.rows_per > 1 ? 3 * p.dim * (int)sizeof(float) : 0;
+    block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks>
+        <<<blocks, threads, smem, stream>>>(p, m);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(p.weight || p.res_scale || p.next_weight)) return e;
-    block_norm_reduce_kernel<<<dim3((unsigned)((p.dim + 31) / 32), 3), 256, 0, stream>>>(
-        p.partial, blocks * m.rows_per, p.dim, p.weight ? p.dweight : nullptr,
+    block_norm_reduce_kernel<<<dim3((unsigned)((p.dim + 31) / 32), 3), 1024, 0, stream>>>(
+        p.partial, blocks, p.dim, p.weight ? p.dweight : nullptr,
         p.res_scale ? p.dres_scale : nullptr, p.next_weight ? p.dnext_weight : nullptr);
     return cudaGetLastError();
 }
@@ -452,23 +541,25 @@ template <typename T, typename TR>
 cudaError_t bwd_typed(const BlockNormParams &p, cudaStream_t stream) {
     Map m;
     if (use_vec(p)) {
-        if (fits(p, 8, 1, 512, &m)) return bwd<T, TR, 8, 1, 512>(p, m, stream);
-        if (fits(p, 8, 2, 512, &m)) return bwd<T, TR, 8, 2, 512>(p, m, stream);
-        if (fits(p, 8, 4, 1024, &m)) return bwd<T, TR, 8, 4, 1024>(p, m, stream);
+        if (fits(p, 8, 1, 320, &m)) return bwd<T, TR, 8, 1, 320, 2>(p, m, stream);
+        if (fits(p, 8, 1, 640, &m)) return bwd<T, TR, 8, 1, 640, 1>(p, m, stream);
+        if (fits(p, 8, 2, 512, &m)) return bwd<T, TR, 8, 2, 512, 1>(p, m, stream);
+        if (fits(p, 8, 4, 512, &m)) return bwd<T, TR, 8, 4, 512, 1>(p, m, stream);
     }
-    if (fits(p, 1, 4, 512, &m)) return bwd<T, TR, 1, 4, 512>(p, m, stream);
-    if (fits(p, 1, 16, 512, &m)) return bwd<T, TR, 1, 16, 512>(p, m, stream);
-    if (fits(p, 1, 32, 1024, &m)) return bwd<T, TR, 1, 32, 1024>(p, m, stream);
+    if (fits(p, 1, 4, 512, &m)) return bwd<T, TR, 1, 4, 512, 2>(p, m, stream);
+    if (fits(p, 1, 16, 512, &m)) return bwd<T, TR, 1, 16, 512, 1>(p, m, stream);
+    if (fits(p, 1, 32, 1024, &m)) return bwd<T, TR, 1, 32, 1024, 1>(p, m, stream);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-// Row slots the gradient's blocks keep column sums for: about a thousand
-// threads an SM at eight columns a thread, two blocks an SM at least.
-int block_norm_bwd_slots(long long rows, int dim) {
-    const long long most = std::max<long long>(2 * 148, 148ll * 8 * 1024 / dim);
-    return (int)std::max<long long>(128, std::min(rows + 127, most));
+// Blocks of the gradient, each with its column sums: about a thousand threads
+// an SM, two blocks at least.
+int block_norm_bwd_blocks(long long rows, int dim, int threads) {
+    (void)dim;
+    const long long most = 148ll * std::max(2, 1024 / std::max(threads, 1));
+    return (int)std::max<long long>(1, std::min(rows, most));
 }
 
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream) {

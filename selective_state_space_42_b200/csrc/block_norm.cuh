@@ -18,7 +18,7 @@ struct BlockNormParams {
     void *out, *y;                      // forward: [rows][dim], each may be NULL
     const void *dout, *dy;              // gradient: [rows][dim], each may be NULL
     void *dx, *dz, *dres;
-    float *partial;                     // [slots][3][dim]: dweight, dres_scale, dnext_weight sums
+    float *partial;                     // [blocks][3][dim]: dweight, dres_scale, dnext_weight sums
     float *dweight, *dres_scale, *dnext_weight;
     long long rows;
     int dim, groups;
@@ -29,6 +29,6 @@ struct BlockNormParams {
 };
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
-int block_norm_bwd_slots(long long rows, int dim);  // sizes `partial`
+int block_norm_bwd_blocks(long long rows, int dim, int threads);  // sizes `partial` (threads a block: 128 at least)
 
 }  // namespace selscan

@@ -692,7 +692,9 @@ SELSCAN_API int64_t selscan_block_norm_bwd_workspace_bytes(int64_t rows, int64_t
  * sequence chunk waited too long for its predecessor's state; 2, 3: a
  * pipeline stage waited too long; 4: a tensor-core MMA or its operand copy
  * of selscan_ssd_fwd did not complete in time; 5: the state copy of a
- * selscan_state_update step did not complete in time). Every device-side wait in the library is
+ * selscan_state_update step did not complete in time; 6: a step of the tensor-core pipeline of
+ * selscan_linattn_fwd or _bwd; 7: a row copy of selscan_block_norm_fwd or _bwd).
+ * Every device-side wait in the library is
  * bounded (2 s); a wait that gives up records its code here and the kernel
  * returns instead of hanging, leaving its outputs undefined. `clear` nonzero
  * resets the word to 0 after reading it.

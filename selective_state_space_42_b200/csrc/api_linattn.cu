@@ -531,7 +531,8 @@ int selscan_block_norm_fwd(const void *x, const selscan_block_norm_options_t *op
     p.out = out;
     p.y = y;
     p.vec = p.vec && !misaligned(out, 16) && !misaligned(y, 16);
-    const cudaError_t e = launch_block_norm_fwd(p, dtype == SELSCAN_BF16, stream);
+    cudaError_t e = device_status_address(&p.status);
+    if (e == cudaSuccess) e = launch_block_norm_fwd(p, dtype == SELSCAN_BF16, stream);
     return e == cudaSuccess ? SELSCAN_OK : cuda_fail(e);
 }
 
@@ -593,7 +594,9 @@ int selscan_block_norm_bwd(const void *x, const selscan_block_norm_options_t *op
     p.partial = static_cast<float *>(ws);
     p.vec = p.vec && !misaligned(dout, 16) && !misaligned(dy, 16) && !misaligned(dx, 16) &&
             !misaligned(dz, 16) && !misaligned(dresidual, 16);
-    return finish(launch_block_norm_bwd(p, dtype == SELSCAN_BF16, stream), ws, !workspace, stream);
+    cudaError_t e = device_status_address(&p.status);
+    if (e == cudaSuccess) e = launch_block_norm_bwd(p, dtype == SELSCAN_BF16, stream);
+    return finish(e, ws, !workspace, stream);
 }
 
 }  // extern "C"

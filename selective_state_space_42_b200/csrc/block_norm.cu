@@ -16,8 +16,11 @@
 // group stay within its threads. All arithmetic and all sums are float32; the
 // only roundings to bfloat16 are the stores.
 #include "block_norm.cuh"
+#include "tma_util.cuh"
 
 #include <algorithm>
+
+#include "api_util.cuh"
 
 namespace selscan {
 namespace {
@@ -88,56 +91,136 @@ struct Map {
     int tg, row_threads, rows_per;
 };
 
-// Sums of a float2 over the threads of this thread's group or row: `threads` is
+// Sums of kN floats over the threads of this thread's group or row: `threads` is
 // a power of two up to a warp, or whole warps starting at a multiple of it (the
 // whole block for a row). Every thread of the block calls it; `red` has a float2
-// per warp, and another call's until two block barriers later.
-__device__ __forceinline__ float2 sum_over(float2 v, int threads, float2 *red) {
+// per warp, and another call's until two block barriers later. Behind the barrier
+// every warp adds the warps' sums by shuffles again (one shared-memory read a
+// lane; reading them one after another took 0.4 µs a sum at 20 warps).
+template <int kN>
+__device__ __forceinline__ void sum_over(float (&v)[kN], int threads, float2 *red) {
     if (threads <= 32) {
-        for (int m = threads >> 1; m > 0; m >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-        }
-        return v;
+        for (int m = threads >> 1; m > 0; m >>= 1)
+#pragma unroll
+            for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+        return;
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-    }
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[w] = v;
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[w] = make_float2(v[0], v[kN - 1]);
     __syncthreads();
     const int per = threads >> 5, first = w / per * per;
-    float2 s = make_float2(0.f, 0.f);
-    for (int k = 0; k < per; ++k) {
-        const float2 r = red[first + k];
-        s.x += r.x;
-        s.y += r.y;
-    }
-    return s;
+    const float2 r = lane < per ? red[first + lane] : make_float2(0.f, 0.f);
+    v[0] = r.x;
+    if (kN > 1) v[kN - 1] = r.y;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
 }
 
-template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
+// ---- rows through shared memory -------------------------------------------------------
+// With many rows a block, each row's operands come by bulk copies into a ring of
+// stages, several rows ahead, so that the memory system stays busy through the
+// sums' barriers. All threads read a stage at a row's start, thread 0 refills it
+// after the first barrier behind that.
+constexpr int kMaxStages = 8;
+constexpr uint64_t kRowWaitNs = 2000000000ull;  // a copy that takes longer is given up
+constexpr int kStatusRowCopy = 7;                // device error code
+__device__ const int kNoAbortRow = 0;
+
+__device__ __forceinline__ void bulk_row(void *dst, const void *src, uint32_t bytes,
+                                         uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Thread 0: row `row` into a stage.
+template <typename T, typename TR>
+__device__ __forceinline__ void fetch_row(const BlockNormParams &p, unsigned char *stage,
+                                          uint64_t *bar, long long row, bool bwd) {
+    const uint32_t nt = (uint32_t)p.dim * sizeof(T), nr = (uint32_t)p.dim * sizeof(TR);
+    const bool z = p.gate != kGateNone, res = p.res && (!bwd || p.next_weight),
+               dy = bwd && p.next_weight, dout = bwd && p.dout;
+    mbar_arrive_expect_tx(bar, nt * (1 + z + dy) + nr * (res + dout));
+    bulk_row(stage, static_cast<const T *>(p.x) + row * p.x_row, nt, bar);
+    if (z) bulk_row(stage + p.off_z, static_cast<const T *>(p.z) + row * p.z_row, nt, bar);
+    if (res) bulk_row(stage + p.off_res, static_cast<const TR *>(p.res) + row * p.dim, nr, bar);
+    if (dy) bulk_row(stage + p.off_dy, static_cast<const T *>(p.dy) + row * p.dim, nt, bar);
+    if (dout) bulk_row(stage + p.off_dout, static_cast<const TR *>(p.dout) + row * p.dim, nr, bar);
+}
+
+// A copy did not come in time: it is recorded, and the block goes once the copies
+// still on their way have landed (or been given up too).
+__device__ __noinline__ void row_copy_failed(const BlockNormParams &p, uint64_t *full, int stage,
+                                             uint32_t phase, long long base) {
+    if (threadIdx.x == 0) {
+        if (p.status) atomicCAS(p.status, 0, kStatusRowCopy);
+        for (int k = 0; k < p.stages && base + (long long)k * gridDim.x < p.rows; ++k) {
+            mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs);
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks, bool kRing>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     __shared__ float2 red[2][32];
+    __shared__ uint64_t full[kMaxStages];
+    extern __shared__ __align__(128) unsigned char dyn[];
     const int t = threadIdx.x, local = t % m.row_threads;
-    const long long row = (long long)blockIdx.x * m.rows_per + t / m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
+    if (kRing) {
+        if (t == 0) {
+            for (int k = 0; k < p.stages; ++k) mbar_init(&full[k], 1);
+            fence_barrier_init();
+            for (int k = 0; k < p.stages; ++k) {
+                const long long r = blockIdx.x + (long long)k * gridDim.x;
+                if (r < p.rows)
+                    fetch_row<T, TR>(p, dyn + (size_t)k * p.stage_bytes, &full[k], r, false);
+            }
+        }
+        __syncthreads();
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+    for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
+         base += (long long)gridDim.x * m.rows_per) {
+    const long long row = base + t / m.row_threads;
     const bool live = row < p.rows && grp < p.groups;
+    unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
+    if (kRing && __syncthreads_or(!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs))) {
+        row_copy_failed(p, full, stage, phase, base);
+        return;
+    }
     Raw<T, kVec> x[kNV], z[kNV];
     Raw<TR, kVec> res[kNV];
     float v[kNV][kVec];
-    float sum = 0.f;
+    float sum[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
         if (!live || e >= gs) continue;
         const long long c = (long long)grp * gs + e;
-        x[i].ld(p.x, row * p.x_row + c);
-        if (p.gate != kGateNone) z[i].ld(p.z, row * p.z_row + c);
-        if (p.res) res[i].ld(p.res, row * p.dim + c);
+        if (kRing) {
+            x[i].ld(at, c);
+            if (p.gate != kGateNone) z[i].ld(at + p.off_z, c);
+            if (p.res) res[i].ld(at + p.off_res, c);
+        } else {
+            x[i].ld(p.x, row * p.x_row + c);
+            if (p.gate != kGateNone) z[i].ld(p.z, row * p.z_row + c);
+            if (p.res) res[i].ld(p.res, row * p.dim + c);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -151,12 +234,23 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(g[k]);
         }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) sum = fmaf(v[i][k], v[i][k], sum);
+        for (int k = 0; k < kVec; ++k) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
     }
     float rstd = 1.f;
-    if (p.weight)
-        rstd = rsqrtf(sum_over(make_float2(sum, 0.f), m.tg, red[0]).x / (float)gs + p.eps);
-    float sum2 = 0.f;
+    if (p.weight) {
+        sum_over(sum, m.tg, red[0]);
+        rstd = rsqrtf(sum[0] / (float)gs + p.eps);
+    }
+    if (kRing) {
+        if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
+        const long long next = base + (long long)p.stages * gridDim.x;
+        if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, false);
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    float sum2[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
@@ -184,12 +278,12 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             for (int k = 0; k < kVec; ++k) v[i][k] += f[k];
         }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) sum2 = fmaf(v[i][k], v[i][k], sum2);
+        for (int k = 0; k < kVec; ++k) sum2[0] = fmaf(v[i][k], v[i][k], sum2[0]);
         if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
     }
-    if (!p.next_weight) return;
-    const float rstd2 =
-        rsqrtf(sum_over(make_float2(sum2, 0.f), m.row_threads, red[1]).x / (float)p.dim + p.eps);
+    if (!p.next_weight) continue;
+    sum_over(sum2, m.row_threads, red[1]);
+    const float rstd2 = rsqrtf(sum2[0] / (float)p.dim + p.eps);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
@@ -200,6 +294,7 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
 #pragma unroll
         for (int k = 0; k < kVec; ++k) v[i][k] *= rstd2 * w[k];
         Raw<T, kVec>::st(p.y, row * p.dim + c, v[i]);
+    }
     }
 }
 
@@ -213,11 +308,13 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
 // Everything of the forward is recomputed from the inputs. Blocks stride over
 // the rows and keep the three column sums of their rows in registers; a
 // second kernel adds the blocks' sums in a fixed order.
-template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
+template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks, bool kRing>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
-    __shared__ float2 red[3][32];
-    extern __shared__ float sums[];  // [3][dim] where a block has several rows
+    __shared__ float2 reds[2][3][32];  // of rows in turn: a row may have a single barrier
+    __shared__ uint64_t full[kMaxStages];
+    extern __shared__ __align__(128) unsigned char dyn[];
+    float *sums = reinterpret_cast<float *>(dyn);  // [3][dim] where a block has several rows
     const int t = threadIdx.x, local = t % m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
     const int sub = t / m.row_threads;
@@ -227,11 +324,31 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) aw[i][k] = as[i][k] = an[i][k] = 0.f;
-
+    if (kRing) {
+        if (t == 0) {
+            for (int k = 0; k < p.stages; ++k) mbar_init(&full[k], 1);
+            fence_barrier_init();
+            for (int k = 0; k < p.stages; ++k) {
+                const long long r = blockIdx.x + (long long)k * gridDim.x;
+                if (r < p.rows)
+                    fetch_row<T, TR>(p, dyn + (size_t)k * p.stage_bytes, &full[k], r, true);
+            }
+        }
+        __syncthreads();
+    }
+    int stage = 0;
+    uint32_t phase = 0, odd = 0;
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
          base += (long long)gridDim.x * m.rows_per) {
         const long long row = base + sub;
         const bool live = row < p.rows && grp < p.groups;
+        float2(*red)[32] = reds[odd];
+        odd ^= 1;
+        unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
+        if (kRing && __syncthreads_or(!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs))) {
+            row_copy_failed(p, full, stage, phase, base);
+            return;
+        }
         Raw<T, kVec> xr[kNV], zr[kNV], yr[kNV];
         Raw<TR, kVec> rr[kNV], dr[kNV];
 #pragma unroll
@@ -239,13 +356,21 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             const int e = (i * m.tg + lane) * kVec;
             if (!live || e >= gs) continue;
             const long long c = (long long)grp * gs + e;
-            xr[i].ld(p.x, row * p.x_row + c);
-            if (p.gate != kGateNone) zr[i].ld(p.z, row * p.z_row + c);
-            if (p.res && p.next_weight) rr[i].ld(p.res, row * p.dim + c);
-            if (p.next_weight) yr[i].ld(p.dy, row * p.dim + c);
-            if (p.dout) dr[i].ld(p.dout, row * p.dim + c);
+            if (kRing) {
+                xr[i].ld(at, c);
+                if (p.gate != kGateNone) zr[i].ld(at + p.off_z, c);
+                if (p.res && p.next_weight) rr[i].ld(at + p.off_res, c);
+                if (p.next_weight) yr[i].ld(at + p.off_dy, c);
+                if (p.dout) dr[i].ld(at + p.off_dout, c);
+            } else {
+                xr[i].ld(p.x, row * p.x_row + c);
+                if (p.gate != kGateNone) zr[i].ld(p.z, row * p.z_row + c);
+                if (p.res && p.next_weight) rr[i].ld(p.res, row * p.dim + c);
+                if (p.next_weight) yr[i].ld(p.dy, row * p.dim + c);
+                if (p.dout) dr[i].ld(p.dout, row * p.dim + c);
+            }
         }
-        float sum = 0.f;
+        float sum[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
@@ -258,14 +383,25 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 for (int k = 0; k < kVec; ++k) x[k] *= silu_f32(z[k]);
             }
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) sum = fmaf(x[k], x[k], sum);
+            for (int k = 0; k < kVec; ++k) sum[0] = fmaf(x[k], x[k], sum[0]);
         }
         float rstd = 1.f;
-        if (p.weight)
-            rstd = rsqrtf(sum_over(make_float2(sum, 0.f), m.tg, red[0]).x / (float)gs + p.eps);
+        if (p.weight) {
+            sum_over(sum, m.tg, red[0]);
+            rstd = rsqrtf(sum[0] / (float)gs + p.eps);
+        }
+        if (kRing) {
+            if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
+            const long long next = base + (long long)p.stages * gridDim.x;
+            if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, true);
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
         // out, its norm's statistics
         float r[kNV][kVec];
-        float2 s2 = make_float2(0.f, 0.f);
+        float s2[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
@@ -298,17 +434,17 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             ld_weight<kVec>(p.next_weight, c, f);
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                s2.x = fmaf(r[i][k], r[i][k], s2.x);
-                s2.y = fmaf(dy[k] * f[k], r[i][k], s2.y);
+                s2[0] = fmaf(r[i][k], r[i][k], s2[0]);
+                s2[1] = fmaf(dy[k] * f[k], r[i][k], s2[1]);
             }
         }
         float rstd2 = 1.f, coef = 0.f;
         if (p.next_weight) {
-            s2 = sum_over(s2, m.row_threads, red[1]);
-            rstd2 = rsqrtf(s2.x / (float)p.dim + p.eps);
-            coef = s2.y * rstd2 / (float)p.dim;
+            sum_over(s2, m.row_threads, red[1]);
+            rstd2 = rsqrtf(s2[0] / (float)p.dim + p.eps);
+            coef = s2[1] * rstd2 / (float)p.dim;
         }
-        float s_dn = 0.f;
+        float s_dn[1] = {0.f};
         float d[kNV][kVec];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
@@ -372,12 +508,15 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 for (int k = 0; k < kVec; ++k) {
                     aw[i][k] = fmaf(d[i][k], n[k], aw[i][k]);
                     d[i][k] *= w[k];
-                    s_dn = fmaf(d[i][k], n[k], s_dn);
+                    s_dn[0] = fmaf(d[i][k], n[k], s_dn[0]);
                 }
             }
         }
         float cg = 0.f;
-        if (p.weight) cg = sum_over(make_float2(s_dn, 0.f), m.tg, red[2]).x / (float)gs;
+        if (p.weight) {
+            sum_over(s_dn, m.tg, red[2]);
+            cg = s_dn[0] / (float)gs;
+        }
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
@@ -500,11 +639,47 @@ bool fits(const BlockNormParams &p, int vec, int nv, int threads, Map *m) {
 
 bool use_vec(const BlockNormParams &p) { return p.vec && (p.dim / p.groups) % 8 == 0; }
 
+// The ring for a block's rows: stage layout, and as many stages (up to eight) as
+// `room` bytes hold; 0 where fewer than two fit or a block has fewer than
+// `enough` rows to bring.
+int plan_ring(BlockNormParams *p, size_t es, size_t rs, bool bwd, long long blocks, int room) {
+    const int nt = (int)(p->dim * es), nr = (int)(p->dim * rs);
+    int off = nt;
+    auto take = [&off](bool have, int n) {
+        const int at = off;
+        if (have) off += n;
+        return at;
+    };
+    p->off_z = take(p->gate != kGateNone, nt);
+    p->off_res = take(p->res && (!bwd || p->next_weight), nr);
+    p->off_dy = take(bwd && p->next_weight, nt);
+    p->off_dout = take(bwd && p->dout, nr);
+    p->stage_bytes = (off + 127) / 128 * 128;
+    p->stages = std::min(room / p->stage_bytes, kMaxStages);
+    if (p->stages < 2 || p->rows < 4 * blocks) p->stages = 0;
+    return p->stages;
+}
+
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
-cudaError_t fwd(const BlockNormParams &p, const Map &m, cudaStream_t stream) {
+cudaError_t fwd(const BlockNormParams &params, const Map &m, cudaStream_t stream) {
+    BlockNormParams p = params;
+    const int threads = m.row_threads * m.rows_per;
+    if constexpr (kVec == 8) {
+        // two blocks an SM, 100 KB of rows on their way to each
+        const long long blocks = 2ll * sm_count();
+        if (m.rows_per == 1 && plan_ring(&p, sizeof(T), sizeof(TR), false, blocks, 100 << 10)) {
+            auto k = block_norm_fwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, true>;
+            const int smem = p.stages * p.stage_bytes;
+            const cudaError_t e =
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            k<<<(unsigned)blocks, threads, smem, stream>>>(p, m);
+            return cudaGetLastError();
+        }
+    }
     const long long blocks = (p.rows + m.rows_per - 1) / m.rows_per;
-    block_norm_fwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks>
-        <<<(unsigned)blocks, m.row_threads * m.rows_per, 0, stream>>>(p, m);
+    block_norm_fwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, false>
+        <<<(unsigned)blocks, threads, 0, stream>>>(p, m);
     return cudaGetLastError();
 }
 
@@ -522,17 +697,36 @@ cudaError_t fwd_typed(const BlockNormParams &p, cudaStream_t stream) {
 }
 
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
-cudaError_t bwd(const BlockNormParams &p, const Map &m, cudaStream_t stream) {
+cudaError_t bwd(const BlockNormParams &params, const Map &m, cudaStream_t stream) {
+    BlockNormParams p = params;
     const long long want = (p.rows + m.rows_per - 1) / m.rows_per;
     const int threads = m.row_threads * m.rows_per;
-    const int blocks = (int)std::min<long long>(want, block_norm_bwd_blocks(p.rows, p.dim, std::max(threads, 128)));
-    const int smem = m.rows_per > 1 ? 3 * p.dim * (int)sizeof(float) : 0;
-    block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks>
-        <<<blocks, threads, smem, stream>>>(p, m);
+    long long blocks =
+        std::min<long long>(want, block_norm_bwd_blocks(p.rows, p.dim, std::max(threads, 128)));
+    bool ring = false;
+    if constexpr (kVec == 8) {
+        const long long two = (long long)kBlocks * sm_count();
+        if (m.rows_per == 1 && two <= blocks &&
+            plan_ring(&p, sizeof(T), sizeof(TR), true, two, kBlocks == 2 ? 100 << 10 : 200 << 10)) {
+            ring = true;
+            blocks = two;
+            auto k = block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, true>;
+            const int smem = p.stages * p.stage_bytes;
+            const cudaError_t e =
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            k<<<(unsigned)blocks, threads, smem, stream>>>(p, m);
+        }
+    }
+    if (!ring) {
+        const int smem = m.rows_per > 1 ? 3 * p.dim * (int)sizeof(float) : 0;
+        block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, false>
+            <<<(unsigned)blocks, threads, smem, stream>>>(p, m);
+    }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(p.weight || p.res_scale || p.next_weight)) return e;
     block_norm_reduce_kernel<<<dim3((unsigned)((p.dim + 31) / 32), 3), 1024, 0, stream>>>(
-        p.partial, blocks, p.dim, p.weight ? p.dweight : nullptr,
+        p.partial, (int)blocks, p.dim, p.weight ? p.dweight : nullptr,
         p.res_scale ? p.dres_scale : nullptr, p.next_weight ? p.dnext_weight : nullptr);
     return cudaGetLastError();
 }

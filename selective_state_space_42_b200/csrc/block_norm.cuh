@@ -26,6 +26,10 @@ struct BlockNormParams {
     int res_f32;                        // type of res, out, dout, dres (else the I/O type)
     int vec;                            // every row starts on a 16-byte boundary
     float eps;
+    // rows brought through a ring of shared-memory stages (set by the launcher): bytes
+    // of a stage, where z, res, dy and dout stand in it
+    int stages, stage_bytes, off_z, off_res, off_dy, off_dout;
+    int *status;                        // the library's device error word
 };
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);

@@ -6,7 +6,7 @@ from __future__ import annotations
 import ctypes
 
 from . import selscan as _s
-from .linattn import _on
+from .linattn import _dense, _on, _raw_stream
 from .selscan import BlockNormOptions, _check, _dtype_code, _ptr, _torch
 
 GATES = {"before": 1, "after": 2}
@@ -15,14 +15,15 @@ GATES = {"before": 1, "after": 2}
 def _flat(t, name, shape, dtype, device):
     """Pointer and elements between rows of a [..., dim] operand with evenly
     spaced rows."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr(), 0
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
     dim = shape[-1]
     # rows evenly spaced: every leading stride is the next one times its size
     row = None
@@ -61,11 +62,12 @@ def _options(x, z, weight, residual, res_scale, next_weight, groups, eps, gate, 
     f32 = torch.float32
     xp, xs = _flat(x, "x", shape, dt, dev)
     zp, zs = (None, 0) if z is None else _flat(z, "z", shape, dt, dev)
+    row = (dim,)
     opts = BlockNormOptions(
-        zp, xs, zs, _ptr(weight, "weight", (dim,), f32, dev, required=False),
-        _ptr(residual, "residual", shape, rt, dev, required=False),
-        _ptr(res_scale, "res_scale", (dim,), f32, dev, required=False),
-        _ptr(next_weight, "next_weight", (dim,), f32, dev, required=False),
+        zp, xs, zs, None if weight is None else _dense(weight, "weight", row, f32, dev),
+        None if residual is None else _dense(residual, "residual", shape, rt, dev),
+        None if res_scale is None else _dense(res_scale, "res_scale", row, f32, dev),
+        None if next_weight is None else _dense(next_weight, "next_weight", row, f32, dev),
         groups, 0 if z is None else GATES[gate], int(rt == f32), eps)
     rows = x.numel() // dim if dim else 0
     return xp, opts, rt, rows, dim, code
@@ -91,13 +93,13 @@ def selscan_block_norm_fwd(x, z=None, weight=None, residual=None, res_scale=None
     dev = x.device
     with _on(dev, stream, (x, z, weight, residual, res_scale, next_weight, out, y)):
         if out is None:
-            out = torch.empty(x.shape, device=dev, dtype=rt)
+            out = torch.empty_like(x, dtype=rt, memory_format=torch.contiguous_format)
         if y is None and next_weight is not None:
-            y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
         _check(_s.load_library().selscan_block_norm_fwd(
-            xp, ctypes.byref(opts), _ptr(out, "out", x.shape, rt, dev),
-            _ptr(y, "y", x.shape, x.dtype, dev, required=False), rows, dim, code,
-            torch.cuda.current_stream(dev).cuda_stream))
+            xp, ctypes.byref(opts), _dense(out, "out", x.shape, rt, dev),
+            None if y is None else _dense(y, "y", x.shape, x.dtype, dev), rows, dim, code,
+            _raw_stream(dev)))
     return out, y
 
 
@@ -115,7 +117,8 @@ def selscan_block_norm_bwd(x, z=None, weight=None, residual=None, res_scale=None
     dev, f32 = x.device, torch.float32
     with _on(dev, stream, (x, z, weight, residual, res_scale, next_weight, dout, dy)):
         def like(t, dtype):
-            return None if t is None else torch.empty(t.shape, device=dev, dtype=dtype)
+            return None if t is None else torch.empty_like(
+                t, dtype=dtype, memory_format=torch.contiguous_format)
 
         out = dict(dx=like(x, x.dtype), dz=like(z, x.dtype), dresidual=like(residual, rt),
                    dweight=like(weight, f32), dres_scale=like(res_scale, f32),
@@ -123,9 +126,10 @@ def selscan_block_norm_bwd(x, z=None, weight=None, residual=None, res_scale=None
         nbytes = int(_s.load_library().selscan_block_norm_bwd_workspace_bytes(rows, dim))
         ws = torch.empty(nbytes, device=dev, dtype=torch.uint8) if nbytes else None
         _check(_s.load_library().selscan_block_norm_bwd(
-            xp, ctypes.byref(opts), _ptr(dout, "dout", x.shape, rt, dev, required=False),
-            _ptr(dy, "dy", x.shape, x.dtype, dev, required=False),
+            xp, ctypes.byref(opts),
+            None if dout is None else _dense(dout, "dout", x.shape, rt, dev),
+            None if dy is None else _dense(dy, "dy", x.shape, x.dtype, dev),
             *(None if t is None else t.data_ptr() for t in out.values()), rows, dim, code,
             ws.data_ptr() if nbytes else None, nbytes,
-            torch.cuda.current_stream(dev).cuda_stream))
+            _raw_stream(dev)))
     return out

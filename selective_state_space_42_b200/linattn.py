@@ -10,6 +10,24 @@ from functools import lru_cache
 from . import selscan as _s
 from .selscan import LinattnOptions, _check, _dtype_code, _ptr, _torch
 
+_NO_CONTEXT = nullcontext()
+
+
+def _dense(t, name, shape, dtype, device):
+    """Pointer of a required dense operand; the checks in the order in which
+    they are cheap (a decode step's call is bound by its host time)."""
+    if t is not None and t.shape == shape and t.dtype is dtype and t.is_contiguous() \
+            and t.device == device:
+        return t.data_ptr()
+    return _ptr(t, name, shape, dtype, device)  # says what is wrong
+
+
+def _raw_stream(device):
+    """Handle of the device's current stream."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device.index) if get else torch.cuda.current_stream(device).cuda_stream
+
 
 def _on(device, stream, tensors):
     """Context in which allocations and the launch belong to ``stream`` (None:
@@ -19,7 +37,7 @@ def _on(device, stream, tensors):
     torch = _torch()
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return nullcontext()
+            return _NO_CONTEXT
         return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device)
@@ -37,6 +55,9 @@ def _rows(t, name, shape, dtype, device):
     spaced over the batch (a dense tensor, or a slice of a projection)."""
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr(), 0
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype:
@@ -44,8 +65,6 @@ def _rows(t, name, shape, dtype, device):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     B, L, H, d = shape
-    if t.is_contiguous():
-        return t.data_ptr(), 0
     sb, sl, sh, sd = t.stride()
     row = sl if L > 1 else sb if B > 1 else H * d
     if (d > 1 and sd != 1) or (H > 1 and sh != d) or row < H * d \
@@ -88,8 +107,8 @@ def _decays(log_decay, shape, heads, dtype, device):
     if log_decay is None:
         return None, None
     if log_decay.dim() == 1:
-        return None, _ptr(log_decay, "log_decay", (heads,), _torch().float32, device)
-    return _ptr(log_decay, "log_decay", shape, dtype, device), None
+        return None, _dense(log_decay, "log_decay", (heads,), _torch().float32, device)
+    return _dense(log_decay, "log_decay", shape, dtype, device), None
 
 
 def selscan_linattn_fwd(q, k, v, log_decay=None, scale=None, initial_state=None, seqlens=None,
@@ -114,16 +133,16 @@ def selscan_linattn_fwd(q, k, v, log_decay=None, scale=None, initial_state=None,
     scale = dk ** -0.5 if scale is None else float(scale)
     with _on(dev, stream, (q, k, v, log_decay, initial_state, seqlens, y, final_state)):
         if y is None:
-            y = torch.empty(B, L, H, dv, device=dev, dtype=q.dtype)
+            y = torch.empty_like(v, memory_format=torch.contiguous_format)
         if final_state is None and return_final_state:
             final_state = torch.empty(B, H, dk, dv, device=dev, dtype=torch.float32)
         nbytes = _workspace("selscan_linattn_workspace_bytes", dev.index, *sizes, code)
         ws = torch.empty(nbytes, device=dev, dtype=torch.uint8) if nbytes else None
         _check(_s.load_library().selscan_linattn_fwd(
-            *ptrs, scale, ctypes.byref(opts), _ptr(y, "y", (B, L, H, dv), q.dtype, dev),
+            *ptrs, scale, ctypes.byref(opts), _dense(y, "y", (B, L, H, dv), q.dtype, dev),
             _ptr(final_state, "final_state", (B, H, dk, dv), torch.float32, dev, required=False),
             *sizes, code, ws.data_ptr() if nbytes else None, nbytes,
-            torch.cuda.current_stream(dev).cuda_stream))
+            _raw_stream(dev)))
     return (y, final_state) if return_final_state else y
 
 
@@ -152,12 +171,12 @@ def selscan_linattn_bwd(q, k, v, log_decay=None, scale=None, initial_state=None,
         nbytes = _workspace("selscan_linattn_bwd_workspace_bytes", dev.index, *sizes, code)
         ws = torch.empty(nbytes, device=dev, dtype=torch.uint8) if nbytes else None
         _check(_s.load_library().selscan_linattn_bwd(
-            *ptrs, scale, ctypes.byref(opts), _ptr(dy, "dy", (B, L, H, dv), dt, dev),
+            *ptrs, scale, ctypes.byref(opts), _dense(dy, "dy", (B, L, H, dv), dt, dev),
             _ptr(dfinal_state, "dfinal_state", (B, H, dk, dv), torch.float32, dev, required=False),
             *(None if out[n] is None else out[n].data_ptr()
               for n in ("dq", "dk", "dv", "dlog_decay", "dh0")),
             *sizes, code, ws.data_ptr() if nbytes else None, nbytes,
-            torch.cuda.current_stream(dev).cuda_stream))
+            _raw_stream(dev)))
     return out
 
 
@@ -167,7 +186,9 @@ def selscan_linattn_step(state, q, k, v, log_decay=None, scale=None, y=None, str
     qk_heads, dk]; v: [batch, heads, dv]; log_decay: [batch, heads] of q's
     dtype, or [heads] float32, or None. Returns y [batch, heads, dv]."""
     torch = _torch()
-    if state.dim() != 4 or q.dim() != 3:
+    if state.dim() != 4 or q.dim() != 3 or not q.is_cuda:
+        if state.dim() == 4 and q.dim() == 3:
+            raise ValueError("q must be a CUDA tensor")
         raise ValueError("state must be [batch, heads, dk, dv] and q [batch, qk_heads, dk]")
     B, H, dk, dv = state.shape
     Hq = q.shape[1]
@@ -177,11 +198,11 @@ def selscan_linattn_step(state, q, k, v, log_decay=None, scale=None, y=None, str
     per_token, per_head = _decays(log_decay, (B, H), H, dt, dev)
     with _on(dev, stream, (state, q, k, v, log_decay, y)):
         if y is None:
-            y = torch.empty(B, H, dv, device=dev, dtype=dt)
+            y = torch.empty_like(v)
         _check(_s.load_library().selscan_linattn_step(
-            _ptr(state, "state", (B, H, dk, dv), torch.float32, dev),
-            _ptr(q, "q", (B, Hq, dk), dt, dev), _ptr(k, "k", (B, Hq, dk), dt, dev),
-            _ptr(v, "v", (B, H, dv), dt, dev), per_token, per_head, scale,
-            _ptr(y, "y", (B, H, dv), dt, dev), B, Hq, H, dk, dv, code,
-            torch.cuda.current_stream(dev).cuda_stream))
+            _dense(state, "state", (B, H, dk, dv), torch.float32, dev),
+            _dense(q, "q", (B, Hq, dk), dt, dev), _dense(k, "k", (B, Hq, dk), dt, dev),
+            _dense(v, "v", (B, H, dv), dt, dev), per_token, per_head, scale,
+            _dense(y, "y", (B, H, dv), dt, dev), B, Hq, H, dk, dv, code,
+            _raw_stream(dev)))
     return y

@@ -93,12 +93,12 @@ struct Map {
 
 // Sums of kN floats over the threads of this thread's group or row: `threads` is
 // a power of two up to a warp, or whole warps starting at a multiple of it (the
-// whole block for a row). Every thread of the block calls it; `red` has a float2
+// whole block for a row); `first` is its first warp. Every thread of the block calls it; `red` has a float2
 // per warp, and another call's until two block barriers later. Behind the barrier
 // every warp adds the warps' sums by shuffles again (one shared-memory read a
 // lane; reading them one after another took 0.4 µs a sum at 20 warps).
 template <int kN>
-__device__ __forceinline__ void sum_over(float (&v)[kN], int threads, float2 *red) {
+__device__ __forceinline__ void sum_over(float (&v)[kN], int threads, int first, float2 *red) {
     if (threads <= 32) {
         for (int m = threads >> 1; m > 0; m >>= 1)
 #pragma unroll
@@ -112,8 +112,7 @@ __device__ __forceinline__ void sum_over(float (&v)[kN], int threads, float2 *re
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[w] = make_float2(v[0], v[kN - 1]);
     __syncthreads();
-    const int per = threads >> 5, first = w / per * per;
-    const float2 r = lane < per ? red[first + lane] : make_float2(0.f, 0.f);
+    const float2 r = lane < threads >> 5 ? red[first + lane] : make_float2(0.f, 0.f);
     v[0] = r.x;
     if (kN > 1) v[kN - 1] = r.y;
 #pragma unroll
@@ -175,13 +174,15 @@ __device__ __noinline__ void row_copy_failed(const BlockNormParams &p, uint64_t 
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks, bool kRing>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
-    __shared__ float2 red[2][32];
+    __shared__ float2 reds[2][2][32];  // of rows in turn: a row may have a single barrier
     __shared__ uint64_t full[kMaxStages];
+    __shared__ int failed[2];  // of rows in turn as well
     extern __shared__ __align__(128) unsigned char dyn[];
     const int t = threadIdx.x, local = t % m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
     if (kRing) {
         if (t == 0) {
+            failed[0] = failed[1] = 0;
             for (int k = 0; k < p.stages; ++k) mbar_init(&full[k], 1);
             fence_barrier_init();
             for (int k = 0; k < p.stages; ++k) {
@@ -192,17 +193,18 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         __syncthreads();
     }
+    const float inv_gs = 1.f / (float)gs, inv_dim = 1.f / (float)p.dim;
+    const int first_g = m.tg > 32 ? t / m.tg * (m.tg >> 5) : 0,
+              first_r = t / m.row_threads * (m.row_threads >> 5);
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, odd = 0;
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
          base += (long long)gridDim.x * m.rows_per) {
     const long long row = base + t / m.row_threads;
     const bool live = row < p.rows && grp < p.groups;
+    float2(*red)[32] = reds[odd];
     unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
-    if (kRing && __syncthreads_or(!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs))) {
-        row_copy_failed(p, full, stage, phase, base);
-        return;
-    }
+    if (kRing && !mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
     Raw<T, kVec> x[kNV], z[kNV];
     Raw<TR, kVec> res[kNV];
     float v[kNV][kVec];
@@ -238,11 +240,15 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     }
     float rstd = 1.f;
     if (p.weight) {
-        sum_over(sum, m.tg, red[0]);
-        rstd = rsqrtf(sum[0] / (float)gs + p.eps);
+        sum_over(sum, m.tg, first_g, red[0]);
+        rstd = rsqrtf(sum[0] * inv_gs + p.eps);
     }
     if (kRing) {
         if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
+        if (*(volatile int *)&failed[odd]) {
+            row_copy_failed(p, full, stage, phase, base);
+            return;
+        }
         const long long next = base + (long long)p.stages * gridDim.x;
         if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, false);
         if (++stage == p.stages) {
@@ -250,6 +256,7 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             phase ^= 1;
         }
     }
+    odd ^= 1;
     float sum2[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -282,8 +289,8 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
     }
     if (!p.next_weight) continue;
-    sum_over(sum2, m.row_threads, red[1]);
-    const float rstd2 = rsqrtf(sum2[0] / (float)p.dim + p.eps);
+    sum_over(sum2, m.row_threads, first_r, red[1]);
+    const float rstd2 = rsqrtf(sum2[0] * inv_dim + p.eps);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
         const int e = (i * m.tg + lane) * kVec;
@@ -313,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     __shared__ float2 reds[2][3][32];  // of rows in turn: a row may have a single barrier
     __shared__ uint64_t full[kMaxStages];
+    __shared__ int failed[2];
     extern __shared__ __align__(128) unsigned char dyn[];
     float *sums = reinterpret_cast<float *>(dyn);  // [3][dim] where a block has several rows
     const int t = threadIdx.x, local = t % m.row_threads;
@@ -326,6 +334,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         for (int k = 0; k < kVec; ++k) aw[i][k] = as[i][k] = an[i][k] = 0.f;
     if (kRing) {
         if (t == 0) {
+            failed[0] = failed[1] = 0;
             for (int k = 0; k < p.stages; ++k) mbar_init(&full[k], 1);
             fence_barrier_init();
             for (int k = 0; k < p.stages; ++k) {
@@ -336,6 +345,8 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         __syncthreads();
     }
+    const float inv_gs = 1.f / (float)gs, inv_dim = 1.f / (float)p.dim;
+    const int first_g = m.tg > 32 ? t / m.tg * (m.tg >> 5) : 0, first_r = sub * (m.row_threads >> 5);
     int stage = 0;
     uint32_t phase = 0, odd = 0;
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
@@ -343,12 +354,8 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         const long long row = base + sub;
         const bool live = row < p.rows && grp < p.groups;
         float2(*red)[32] = reds[odd];
-        odd ^= 1;
         unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
-        if (kRing && __syncthreads_or(!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs))) {
-            row_copy_failed(p, full, stage, phase, base);
-            return;
-        }
+        if (kRing && !mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
         Raw<T, kVec> xr[kNV], zr[kNV], yr[kNV];
         Raw<TR, kVec> rr[kNV], dr[kNV];
 #pragma unroll
@@ -387,11 +394,15 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         float rstd = 1.f;
         if (p.weight) {
-            sum_over(sum, m.tg, red[0]);
-            rstd = rsqrtf(sum[0] / (float)gs + p.eps);
+            sum_over(sum, m.tg, first_g, red[0]);
+            rstd = rsqrtf(sum[0] * inv_gs + p.eps);
         }
         if (kRing) {
             if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
+            if (*(volatile int *)&failed[odd]) {
+                row_copy_failed(p, full, stage, phase, base);
+                return;
+            }
             const long long next = base + (long long)p.stages * gridDim.x;
             if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, true);
             if (++stage == p.stages) {
@@ -399,6 +410,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 phase ^= 1;
             }
         }
+        odd ^= 1;
         // out, its norm's statistics
         float r[kNV][kVec];
         float s2[2] = {0.f, 0.f};
@@ -440,9 +452,9 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         float rstd2 = 1.f, coef = 0.f;
         if (p.next_weight) {
-            sum_over(s2, m.row_threads, red[1]);
-            rstd2 = rsqrtf(s2[0] / (float)p.dim + p.eps);
-            coef = s2[1] * rstd2 / (float)p.dim;
+            sum_over(s2, m.row_threads, first_r, red[1]);
+            rstd2 = rsqrtf(s2[0] * inv_dim + p.eps);
+            coef = s2[1] * rstd2 * inv_dim;
         }
         float s_dn[1] = {0.f};
         float d[kNV][kVec];
@@ -514,8 +526,8 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         float cg = 0.f;
         if (p.weight) {
-            sum_over(s_dn, m.tg, red[2]);
-            cg = s_dn[0] / (float)gs;
+            sum_over(s_dn, m.tg, first_g, red[2]);
+            cg = s_dn[0] * inv_gs;
         }
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {

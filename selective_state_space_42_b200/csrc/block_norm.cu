@@ -121,11 +121,34 @@ __device__ __forceinline__ void sum_over(float (&v)[kN], int threads, int first,
         for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
 }
 
+// A sum over the row's threads and one over the group's behind one barrier.
+__device__ __forceinline__ void sum_row_and_group(float &row, float &group, const Map &m,
+                                                  int first_g, float2 *red) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        row += __shfl_xor_sync(0xffffffffu, row, k);
+        const float g = __shfl_xor_sync(0xffffffffu, group, k);
+        if (k < m.tg) group += g;
+    }
+    if (lane == 0) red[w] = make_float2(row, group);
+    __syncthreads();
+    row = lane < m.row_threads >> 5 ? red[lane].x : 0.f;
+    float g = lane < m.tg >> 5 ? red[first_g + lane].y : 0.f;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        row += __shfl_xor_sync(0xffffffffu, row, k);
+        g += __shfl_xor_sync(0xffffffffu, g, k);
+    }
+    if (m.tg > 32) group = g;
+}
+
 // ---- rows through shared memory -------------------------------------------------------
 // With many rows a block, each row's operands come by bulk copies into a ring of
 // stages, several rows ahead, so that the memory system stays busy through the
-// sums' barriers. All threads read a stage at a row's start, thread 0 refills it
-// after the first barrier behind that.
+// sums' barriers. A row's last barrier also serves the next row's first sum, whose
+// operands are read from the next stage a second time: a forward row has one
+// barrier, a gradient's two. Behind it thread 0 refills the row's stage.
 constexpr int kMaxStages = 8;
 constexpr uint64_t kRowWaitNs = 2000000000ull;  // a copy that takes longer is given up
 constexpr int kStatusRowCopy = 7;                // device error code
@@ -154,13 +177,39 @@ __device__ __forceinline__ void fetch_row(const BlockNormParams &p, unsigned cha
     if (dout) bulk_row(stage + p.off_dout, static_cast<const TR *>(p.dout) + row * p.dim, nr, bar);
 }
 
+// A thread's part of the first sum of the row in a stage.
+template <typename T, int kVec, int kNV>
+__device__ __forceinline__ float stage_sum(const BlockNormParams &p, const unsigned char *at,
+                                           bool mine, int grp, int lane, int tg, int gs) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const int e = (i * tg + lane) * kVec;
+        if (!mine || e >= gs) continue;
+        Raw<T, kVec> x;
+        float v[kVec];
+        x.ld(at, grp * gs + e);
+        x.get(v);
+        if (p.gate == kGateBefore) {
+            float g[kVec];
+            x.ld(at + p.off_z, grp * gs + e);
+            x.get(g);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] *= silu_f32(g[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum = fmaf(v[k], v[k], sum);
+    }
+    return sum;
+}
+
 // A copy did not come in time: it is recorded, and the block goes once the copies
 // still on their way have landed (or been given up too).
 __device__ __noinline__ void row_copy_failed(const BlockNormParams &p, uint64_t *full, int stage,
-                                             uint32_t phase, long long base) {
+                                             uint32_t phase, long long base, int copies) {
     if (threadIdx.x == 0) {
         if (p.status) atomicCAS(p.status, 0, kStatusRowCopy);
-        for (int k = 0; k < p.stages && base + (long long)k * gridDim.x < p.rows; ++k) {
+        for (int k = 0; k < copies && base + (long long)k * gridDim.x < p.rows; ++k) {
             mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs);
             if (++stage == p.stages) {
                 stage = 0;
@@ -198,13 +247,24 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
               first_r = t / m.row_threads * (m.row_threads >> 5);
     int stage = 0;
     uint32_t phase = 0, odd = 0;
+    float first[1] = {0.f};  // the row's first sum, where the ring brings it
+    if (kRing) {
+        if (!mbar_wait(&full[0], 0, &kNoAbortRow, kRowWaitNs)) failed[1] = 1;
+        first[0] = stage_sum<T, kVec, kNV>(p, dyn, grp < p.groups, grp, lane, m.tg, gs);
+        sum_over(first, m.tg, first_g, reds[0][1]);
+        __syncthreads();
+        if (failed[1]) {
+            row_copy_failed(p, full, 0, 0, blockIdx.x, p.stages);
+            return;
+        }
+    }
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
          base += (long long)gridDim.x * m.rows_per) {
     const long long row = base + t / m.row_threads;
     const bool live = row < p.rows && grp < p.groups;
     float2(*red)[32] = reds[odd];
+    if (!kRing) odd ^= 1;
     unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
-    if (kRing && !mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
     Raw<T, kVec> x[kNV], z[kNV];
     Raw<TR, kVec> res[kNV];
     float v[kNV][kVec];
@@ -236,27 +296,15 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(g[k]);
         }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
+        for (int k = 0; k < kVec; ++k)
+            if (!kRing) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
     }
     float rstd = 1.f;
     if (p.weight) {
-        sum_over(sum, m.tg, first_g, red[0]);
+        if (kRing) sum[0] = first[0];
+        else sum_over(sum, m.tg, first_g, red[0]);
         rstd = rsqrtf(sum[0] * inv_gs + p.eps);
     }
-    if (kRing) {
-        if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
-        if (*(volatile int *)&failed[odd]) {
-            row_copy_failed(p, full, stage, phase, base);
-            return;
-        }
-        const long long next = base + (long long)p.stages * gridDim.x;
-        if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, false);
-        if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-    odd ^= 1;
     float sum2[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -288,8 +336,30 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         for (int k = 0; k < kVec; ++k) sum2[0] = fmaf(v[i][k], v[i][k], sum2[0]);
         if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
     }
+    if (kRing) {
+        const long long next = base + gridDim.x, later = base + (long long)p.stages * gridDim.x;
+        const int was = stage;
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        first[0] = 0.f;
+        if (next < p.rows) {
+            if (!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
+            if (p.weight)
+                first[0] = stage_sum<T, kVec, kNV>(p, dyn + (size_t)stage * p.stage_bytes,
+                                                   grp < p.groups, grp, lane, m.tg, gs);
+        }
+        sum_row_and_group(sum2[0], first[0], m, first_g, red[0]);
+        if (*(volatile int *)&failed[odd]) {
+            row_copy_failed(p, full, stage, phase, next, p.stages - 1);
+            return;
+        }
+        if (t == 0 && later < p.rows) fetch_row<T, TR>(p, at, &full[was], later, false);
+        odd ^= 1;
+    }
     if (!p.next_weight) continue;
-    sum_over(sum2, m.row_threads, first_r, red[1]);
+    if (!kRing) sum_over(sum2, m.row_threads, first_r, red[1]);
     const float rstd2 = rsqrtf(sum2[0] * inv_dim + p.eps);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -349,13 +419,23 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     const int first_g = m.tg > 32 ? t / m.tg * (m.tg >> 5) : 0, first_r = sub * (m.row_threads >> 5);
     int stage = 0;
     uint32_t phase = 0, odd = 0;
+    float first[1] = {0.f};  // the row's first sum, where the ring brings it
+    if (kRing) {
+        if (!mbar_wait(&full[0], 0, &kNoAbortRow, kRowWaitNs)) failed[1] = 1;
+        first[0] = stage_sum<T, kVec, kNV>(p, dyn, grp < p.groups, grp, lane, m.tg, gs);
+        sum_over(first, m.tg, first_g, reds[0][0]);
+        __syncthreads();
+        if (failed[1]) {
+            row_copy_failed(p, full, 0, 0, blockIdx.x, p.stages);
+            return;
+        }
+    }
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
          base += (long long)gridDim.x * m.rows_per) {
         const long long row = base + sub;
         const bool live = row < p.rows && grp < p.groups;
         float2(*red)[32] = reds[odd];
         unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
-        if (kRing && !mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
         Raw<T, kVec> xr[kNV], zr[kNV], yr[kNV];
         Raw<TR, kVec> rr[kNV], dr[kNV];
 #pragma unroll
@@ -368,7 +448,6 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 if (p.gate != kGateNone) zr[i].ld(at + p.off_z, c);
                 if (p.res && p.next_weight) rr[i].ld(at + p.off_res, c);
                 if (p.next_weight) yr[i].ld(at + p.off_dy, c);
-                if (p.dout) dr[i].ld(at + p.off_dout, c);
             } else {
                 xr[i].ld(p.x, row * p.x_row + c);
                 if (p.gate != kGateNone) zr[i].ld(p.z, row * p.z_row + c);
@@ -381,7 +460,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;
-            if (!live || e >= gs || !p.weight) continue;
+            if (kRing || !live || e >= gs || !p.weight) continue;
             float x[kVec], z[kVec];
             xr[i].get(x);
             if (before) {
@@ -394,23 +473,10 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
         float rstd = 1.f;
         if (p.weight) {
-            sum_over(sum, m.tg, first_g, red[0]);
+            if (kRing) sum[0] = first[0];
+            else sum_over(sum, m.tg, first_g, red[0]);
             rstd = rsqrtf(sum[0] * inv_gs + p.eps);
         }
-        if (kRing) {
-            if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
-            if (*(volatile int *)&failed[odd]) {
-                row_copy_failed(p, full, stage, phase, base);
-                return;
-            }
-            const long long next = base + (long long)p.stages * gridDim.x;
-            if (t == 0 && next < p.rows) fetch_row<T, TR>(p, at, &full[stage], next, true);
-            if (++stage == p.stages) {
-                stage = 0;
-                phase ^= 1;
-            }
-        }
-        odd ^= 1;
         // out, its norm's statistics
         float r[kNV][kVec];
         float s2[2] = {0.f, 0.f};
@@ -465,6 +531,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             const int c = grp * gs + e;
             float f[kVec];
             if (p.dout) {
+                if (kRing) dr[i].ld(at + p.off_dout, c);
                 dr[i].get(d[i]);
             } else {
 #pragma unroll
@@ -472,6 +539,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             }
             if (p.next_weight) {
                 float dy[kVec];
+                if (kRing) yr[i].ld(at + p.off_dy, c);
                 yr[i].get(dy);
                 ld_weight<kVec>(p.next_weight, c, f);
 #pragma unroll
@@ -524,11 +592,34 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 }
             }
         }
-        float cg = 0.f;
-        if (p.weight) {
+        if (kRing) {
+            const long long next = base + gridDim.x, later = base + (long long)p.stages * gridDim.x;
+            const int was = stage;
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            float two[2] = {s_dn[0], 0.f};
+            if (next < p.rows) {
+                if (!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
+                if (p.weight)
+                    two[1] = stage_sum<T, kVec, kNV>(p, dyn + (size_t)stage * p.stage_bytes,
+                                                     grp < p.groups, grp, lane, m.tg, gs);
+            }
+            if (p.weight) sum_over(two, m.tg, first_g, red[2]);
+            if (!p.weight || m.tg <= 32) __syncthreads();  // else the sum's barrier has been
+            if (*(volatile int *)&failed[odd]) {
+                row_copy_failed(p, full, stage, phase, next, p.stages - 1);
+                return;
+            }
+            if (t == 0 && later < p.rows) fetch_row<T, TR>(p, at, &full[was], later, true);
+            s_dn[0] = two[0];
+            first[0] = two[1];
+        } else if (p.weight) {
             sum_over(s_dn, m.tg, first_g, red[2]);
-            cg = s_dn[0] * inv_gs;
         }
+        odd ^= 1;
+        const float cg = s_dn[0] * inv_gs;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const int e = (i * m.tg + lane) * kVec;

@@ -240,6 +240,7 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     uint64_t vp_full[2], vp_empty[2], u_full[2], u_empty[2];
     uint64_t s_full, s_empty, p_full, p_empty, st_full, st_empty;
     uint64_t o_full, o_empty, drain;
+    uint64_t ye_read[4];            // VpOnYe: the strong chunks' outputs are read, in turn
     uint64_t v_sync[2], o_sync;     // the warps of c ◦ V, the output warps
     uint32_t tmem;
     int abort;
@@ -415,6 +416,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         mbar_init(&S.drain, 1);
         mbar_init(&S.o_full, 1);
         mbar_init(&S.o_empty, 4);
+        for (int k = 0; k < 4; ++k) mbar_init(&S.ye_read[k], 4);
         mbar_init(&S.o_sync, 4);
         S.abort = 0;
         fence_barrier_init();
@@ -597,6 +599,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
                            pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
             if (!ok || !wait3(&S.o_empty, (i & 1) ^ 1, &S.st_full, i, &S.p_full, i)) break;
+            // U reads c ◦ V from where this Ye goes
+            if (C::VpOnYe && two && vb && !wait2(&S.vp_empty[vb], i / kVBufs, &S.p_full, i)) break;
             if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (int)C::StParts; ++part)
@@ -684,6 +688,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         const int group = warp >= 16 ? 1 : 0, tg = t - (group ? 512 : 128);
         const int d0 = 32 * (warp & 3), r8 = lane >> 4, c2 = 2 * (lane & 3);
         uint32_t syncs = 0;
+        int strongs = 0;
         for (int i = group; i < n; i += kFull ? 1 : 2) {
             const int s = i % kStages, vb = i % kVBufs, use = i / kVBufs;
             const int nq = min(kC, len - chunk_of(i) * kC);
@@ -737,17 +742,24 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                         }
                     }
                 }
-                if (C::VpOnYe && q == 0 && vb && i > 0 &&
-                    (S.strong[(i - 1) % kSlots] || (i > 1 && S.strong[(i - 2) % kSlots]))) {
-                    ok = wait(&S.o_empty, i - 1);  // a strong chunk's Ye has been read
-                    if (!ok) break;
-                    tc_fence_after();
-                }
                 if (q == 0 && use > 0) {
                     // U has read what stands there
                     ok = wait(kVBufs == kUBufs ? &S.u_full[vb] : &S.vp_empty[vb], use - 1);
                     if (!ok) break;
                     tc_fence_after();
+                }
+                if (C::VpOnYe && q == 0 && vb) {
+                    // The last strong chunk's Ye has been read. U(i − 2) is done, so the
+                    // outputs of chunk i − 4 are: o_empty could be two phases behind, one of
+                    // four barriers that strong chunks take in turn is one behind at most.
+                    const int before = strongs;
+                    strongs += (S.strong[(i - 1) % kSlots] != 0) +
+                               (i > 1 && S.strong[(i - 2) % kSlots] != 0);
+                    if (strongs > before) {
+                        ok = wait(&S.ye_read[(strongs - 1) & 3], (strongs - 1) >> 2);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                 }
                 if (d0 < D) {
 #pragma unroll
@@ -852,6 +864,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         const CUtensorMap *my = &maps.m[a.map_y];
         const bool f32 = kBwd && a.y_f32;
         uint32_t syncs = 0;
+        int strongs = 0;
         for (int i = 0; i < n; ++i) {
             const int s = i % kStages;
             const int t0 = chunk_of(i) * kC, nq = min(kC, len - t0);
@@ -874,6 +887,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 auto done = [&]() {  // the next chunk's products may come
                     tc_fence_before();
                     arrive(&S.o_empty);
+                    if (C::VpOnYe && S.strong[i % kSlots]) arrive(&S.ye_read[strongs++ & 3]);
                 };
                 auto rows = [&](auto is_f32, auto is_dot) {
                     constexpr bool kF32 = decltype(is_f32)::value, kDot = decltype(is_dot)::value;

@@ -221,6 +221,86 @@ def test_captured_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("D,groups,gate,res,parts", [
+    (2560, 1, "after", "f32", {}), (2560, 5, "before", "bf16", {}),
+    (1536, 48, "before", "bf16", {}), (5120, 8, "before", "bf16", {"res": None}),
+    (5120, 1, "after", "f32", {"weight": False}), (10240, 1, "after", "bf16", {"nxt": False}),
+    (2048, 1, "after", "f32", {"weight": False, "nxt": False}), (640, 1, "after", "f32", {"z": False}),
+    (16384, 1, "after", "bf16", {"scale": False}),
+], ids=str)
+def test_many_rows_of_bfloat16(D, groups, gate, res, parts):
+    """Rows enough for several a block, brought in ahead of their use, with every
+    kind of operand there or not."""
+    i, g = make(1301, D, "bf16", D + 1, **{"res": res, **parts})
+    check(i, g, groups=groups, gate=gate, what=f"1301 x {D} {parts}")
+
+
+def test_many_rows_of_slices_captured_and_two_at_once():
+    """x and z of one projection, replayed in a graph on new inputs and run on
+    two streams at a time: the same bits as alone."""
+    R, D = 1400, 2048
+    i, g = make(R, D, "bf16", 12)
+    d = {k: v.to(DEV) for k, v in i.items()}
+    dg = {k: v.to(DEV) for k, v in g.items()}
+    both = torch.cat([d["x"], d["z"]], 1)
+    sliced = {**d, "x": both[:, :D], "z": both[:, D:]}
+
+    def run(a):
+        return [*ss.selscan_block_norm_fwd(**a), *ss.selscan_block_norm_bwd(**a, **dg).values()]
+
+    want = [t.clone() for t in run(d)]
+    for a, b in zip(run(sliced), want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    got = []
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            got += [run(sliced), run(sliced)]
+    torch.cuda.synchronize()
+    for one in got:
+        for a, b in zip(one, want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(sliced)
+    both.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip([t.clone() for t in held], run(sliced)):
+        assert torch.equal(a, b)
+
+
+def test_many_rows_in_place():
+    """out in the residual's place, over rows brought ahead."""
+    i, _ = make(1400, 1024, "bf16", 13, res="bf16")
+    d = {k: v.to(DEV) for k, v in i.items()}
+    out, y = ss.selscan_block_norm_fwd(**d)
+    r = d["residual"].clone()
+    o2, y2 = ss.selscan_block_norm_fwd(**{**d, "residual": r}, out=r)
+    assert o2 is r and torch.equal(r, out) and torch.equal(y2, y)
+
+
+def test_more_rows_than_a_grid_dimension_and_beyond_32_bits():
+    """70001 rows of 8, and rows of slices 2^22 elements apart that pass 2^31."""
+    i, g = make(70001, 8, "bf16", 14)
+    check(i, g, what="70001 x 8")
+    i, g = make(1300, 256, "bf16", 15)
+    d = {k: v.to(DEV) for k, v in i.items()}
+    dg = {k: v.to(DEV) for k, v in g.items()}
+    wide = torch.empty(1300 << 22, device=DEV, dtype=torch.bfloat16)
+    x = wide.as_strided((1300, 256), (1 << 22, 1), 0)
+    z = wide.as_strided((1300, 256), (1 << 22, 1), 1 << 12)
+    x.copy_(d["x"])
+    z.copy_(d["z"])
+    for a, b in zip(ss.selscan_block_norm_fwd(**{**d, "x": x, "z": z}),
+                    ss.selscan_block_norm_fwd(**d)):
+        assert torch.equal(a, b)
+    a = ss.selscan_block_norm_bwd(**{**d, "x": x, "z": z}, **dg)
+    b = ss.selscan_block_norm_bwd(**d, **dg)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_a_block_and_its_gradient(dtype):
     """Norm, linear attention, gated norm and residual sum as a model runs them,

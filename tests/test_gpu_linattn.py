@@ -357,6 +357,109 @@ def test_agrees_with_the_one_group_scan(dtype):
                gh.RTOL[dtype], "scan state")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,d", [(330, 64), (330, 128), (2100, 128), (1500, 48)])
+def test_chunks_of_unlike_decays(dtype, L, d):
+    """Slow and steep stretches that begin and end on chunk edges and inside
+    chunks, with resets among them: each kind of chunk follows each other."""
+    i = make(1, L, 2, 2, d, d, dtype, 21, h0=True, strength=0.05)
+    for a, b in ((64, 128), (192, 200), (250, 320), (640, 896), (1000, 1001)):
+        i["g"][:, a:b] *= 400
+    i["g"][0, 130::97] = -math.inf
+    check_fwd(i, dtype, what="unlike")
+    check_bwd(i, dtype, what="unlike")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [130, 2100])
+def test_fixed_decays_of_every_size(dtype, L):
+    """Fixed decays of nothing, of 1/2 a token, of e^-60 and of a reset at each token."""
+    i = make(1, L, 4, 4, 64, 128, dtype, 22, "fixed", h0=True)
+    i["g"] = torch.tensor([0.0, -0.6931, -60.0, -math.inf])
+    i["v"] *= 0.1
+    check_fwd(i, dtype, what="fixed")
+    check_bwd(i, dtype, what="fixed")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scales(dtype):
+    """A scale is a factor of y and of every gradient; zero gives zeros, and the
+    state has none. Powers of two: the same bits times the factor."""
+    d = dev(make(2, 150, 1, 2, 64, 64, dtype, 23, h0=True))
+    a = (d["q"], d["k"], d["v"], d["g"])
+    kw = dict(initial_state=d["h0"], return_final_state=True)
+    y1, S1 = ss.selscan_linattn_fwd(*a, scale=0.125, **kw)
+    g1 = ss.selscan_linattn_bwd(*a, scale=0.125, initial_state=d["h0"], dy=d["dy"])
+    for f in (-1.0, 2.0, 0.0):
+        y, S = ss.selscan_linattn_fwd(*a, scale=0.125 * f, **kw)
+        g = ss.selscan_linattn_bwd(*a, scale=0.125 * f, initial_state=d["h0"], dy=d["dy"])
+        assert torch.equal(S, S1) and torch.equal(y, y1 * f)
+        for n in ("dq", "dk", "dv", "dh0"):
+            assert torch.equal(g[n], g1[n] * f), (f, n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_heads_and_ragged_rows(dtype):
+    """Heads in groups of four over rows of unequal length, gradients of the
+    shared heads summed in float32."""
+    lens = [0, 130, 61]
+    i = make(3, 130, 2, 8, 64, 128, dtype, 24, h0=True)
+    check_fwd(i, dtype, lens, "shared ragged")
+    check_bwd(i, dtype, lens, "shared ragged")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_calls_at_once(dtype):
+    """Calls on two streams at a time, each with its own workspace, give what
+    they give one after the other."""
+    ds = [dev(make(1, 1900, 2, 2, 128, 128, dtype, s, h0=True)) for s in (25, 26)]
+
+    def run(d, stream):
+        y, S = ss.selscan_linattn_fwd(d["q"], d["k"], d["v"], d["g"], initial_state=d["h0"],
+                                      return_final_state=True, stream=stream)
+        g = ss.selscan_linattn_bwd(d["q"], d["k"], d["v"], d["g"], initial_state=d["h0"],
+                                   dy=d["dy"], dfinal_state=d["dS"], stream=stream)
+        return [y, S, *g.values()]
+
+    want = [[t.clone() for t in run(d, None)] for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = [[], []]
+    for _ in range(3):
+        for n in range(2):
+            with torch.cuda.stream(streams[n]):
+                got[n].append(run(ds[n], None))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for again in got[n]:
+            for a, b in zip(again, want[n]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_rows_than_a_grid_dimension(dtype):
+    check_fwd(make(70001, 1, 1, 1, 8, 8, dtype, 27, h0=True), dtype, what="rows")
+    check_bwd(make(70001, 1, 1, 1, 8, 8, dtype, 28, h0=True), dtype, what="rows")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_beyond_32_bits(dtype):
+    """Slices of tokens 2^22 elements apart: the last ones stand past 2^31."""
+    L, step = 520, 1 << 22
+    i = dev(make(1, L, 1, 1, 64, 64, dtype, 29))
+    wide = torch.empty(L * step, device=DEV, dtype=DT[dtype])
+    at = lambda o: wide.as_strided((1, L, 1, 64), (L * step, step, 64, 1), o)  # noqa: E731
+    q, k, v = at(0), at(64), at(128)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        t.copy_(i[n])
+    assert torch.equal(ss.selscan_linattn_fwd(q, k, v, i["g"]),
+                       ss.selscan_linattn_fwd(i["q"], i["k"], i["v"], i["g"]))
+    a = ss.selscan_linattn_bwd(q, k, v, i["g"], dy=i["dy"])
+    b = ss.selscan_linattn_bwd(i["q"], i["k"], i["v"], i["g"], dy=i["dy"])
+    for n in ("dq", "dk", "dv", "dlog_decay"):
+        assert torch.equal(a[n], b[n]), n
+
+
 def test_no_device_wait_gave_up():
     torch.cuda.synchronize()
     assert ss.selscan_device_status() == 0

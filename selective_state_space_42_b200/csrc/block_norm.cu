@@ -260,118 +260,118 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     }
     for (long long base = (long long)blockIdx.x * m.rows_per; base < p.rows;
          base += (long long)gridDim.x * m.rows_per) {
-    const long long row = base + t / m.row_threads;
-    const bool live = row < p.rows && grp < p.groups;
-    float2(*red)[32] = reds[odd];
-    if (!kRing) odd ^= 1;
-    unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
-    Raw<T, kVec> x[kNV], z[kNV];
-    Raw<TR, kVec> res[kNV];
-    float v[kNV][kVec];
-    float sum[1] = {0.f};
+        const long long row = base + t / m.row_threads;
+        const bool live = row < p.rows && grp < p.groups;
+        float2(*red)[32] = reds[odd];
+        if (!kRing) odd ^= 1;
+        unsigned char *at = dyn + (size_t)stage * p.stage_bytes;
+        Raw<T, kVec> x[kNV], z[kNV];
+        Raw<TR, kVec> res[kNV];
+        float v[kNV][kVec];
+        float sum[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        const int e = (i * m.tg + lane) * kVec;
-        if (!live || e >= gs) continue;
-        const long long c = (long long)grp * gs + e;
-        if (kRing) {
-            x[i].ld(at, c);
-            if (p.gate != kGateNone) z[i].ld(at + p.off_z, c);
-            if (p.res) res[i].ld(at + p.off_res, c);
-        } else {
-            x[i].ld(p.x, row * p.x_row + c);
-            if (p.gate != kGateNone) z[i].ld(p.z, row * p.z_row + c);
-            if (p.res) res[i].ld(p.res, row * p.dim + c);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        const int e = (i * m.tg + lane) * kVec;
-        if (!live || e >= gs) continue;
-        x[i].get(v[i]);
-        if (p.gate == kGateBefore) {
-            float g[kVec];
-            z[i].get(g);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(g[k]);
+        for (int i = 0; i < kNV; ++i) {
+            const int e = (i * m.tg + lane) * kVec;
+            if (!live || e >= gs) continue;
+            const long long c = (long long)grp * gs + e;
+            if (kRing) {
+                x[i].ld(at, c);
+                if (p.gate != kGateNone) z[i].ld(at + p.off_z, c);
+                if (p.res) res[i].ld(at + p.off_res, c);
+            } else {
+                x[i].ld(p.x, row * p.x_row + c);
+                if (p.gate != kGateNone) z[i].ld(p.z, row * p.z_row + c);
+                if (p.res) res[i].ld(p.res, row * p.dim + c);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
-            if (!kRing) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
-    }
-    float rstd = 1.f;
-    if (p.weight) {
-        if (kRing) sum[0] = first[0];
-        else sum_over(sum, m.tg, first_g, red[0]);
-        rstd = rsqrtf(sum[0] * inv_gs + p.eps);
-    }
-    float sum2[1] = {0.f};
+        for (int i = 0; i < kNV; ++i) {
+            const int e = (i * m.tg + lane) * kVec;
+            if (!live || e >= gs) continue;
+            x[i].get(v[i]);
+            if (p.gate == kGateBefore) {
+                float g[kVec];
+                z[i].get(g);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        const int e = (i * m.tg + lane) * kVec;
-        if (!live || e >= gs) continue;
-        const int c = grp * gs + e;
-        float f[kVec];
+                for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(g[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (!kRing) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
+        }
+        float rstd = 1.f;
         if (p.weight) {
-            ld_weight<kVec>(p.weight, c, f);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[i][k] *= rstd * f[k];
+            if (kRing) sum[0] = first[0];
+            else sum_over(sum, m.tg, first_g, red[0]);
+            rstd = rsqrtf(sum[0] * inv_gs + p.eps);
         }
-        if (p.gate == kGateAfter) {
-            z[i].get(f);
+        float sum2[1] = {0.f};
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(f[k]);
-        }
-        if (p.res_scale) {
-            ld_weight<kVec>(p.res_scale, c, f);
+        for (int i = 0; i < kNV; ++i) {
+            const int e = (i * m.tg + lane) * kVec;
+            if (!live || e >= gs) continue;
+            const int c = grp * gs + e;
+            float f[kVec];
+            if (p.weight) {
+                ld_weight<kVec>(p.weight, c, f);
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[i][k] *= f[k];
-        }
-        if (p.res) {
-            res[i].get(f);
+                for (int k = 0; k < kVec; ++k) v[i][k] *= rstd * f[k];
+            }
+            if (p.gate == kGateAfter) {
+                z[i].get(f);
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[i][k] += f[k];
-        }
+                for (int k = 0; k < kVec; ++k) v[i][k] *= silu_f32(f[k]);
+            }
+            if (p.res_scale) {
+                ld_weight<kVec>(p.res_scale, c, f);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) sum2[0] = fmaf(v[i][k], v[i][k], sum2[0]);
-        if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
-    }
-    if (kRing) {
-        const long long next = base + gridDim.x, later = base + (long long)p.stages * gridDim.x;
-        const int was = stage;
-        if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-        }
-        first[0] = 0.f;
-        if (next < p.rows) {
-            if (!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
-            if (p.weight)
-                first[0] = stage_sum<T, kVec, kNV>(p, dyn + (size_t)stage * p.stage_bytes,
-                                                   grp < p.groups, grp, lane, m.tg, gs);
-        }
-        sum_row_and_group(sum2[0], first[0], m, first_g, red[0]);
-        if (*(volatile int *)&failed[odd]) {
-            row_copy_failed(p, full, stage, phase, next, p.stages - 1);
-            return;
-        }
-        if (t == 0 && later < p.rows) fetch_row<T, TR>(p, at, &full[was], later, false);
-        odd ^= 1;
-    }
-    if (!p.next_weight) continue;
-    if (!kRing) sum_over(sum2, m.row_threads, first_r, red[1]);
-    const float rstd2 = rsqrtf(sum2[0] * inv_dim + p.eps);
+                for (int k = 0; k < kVec; ++k) v[i][k] *= f[k];
+            }
+            if (p.res) {
+                res[i].get(f);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        const int e = (i * m.tg + lane) * kVec;
-        if (!live || e >= gs) continue;
-        const int c = grp * gs + e;
-        float w[kVec];
-        ld_weight<kVec>(p.next_weight, c, w);
+                for (int k = 0; k < kVec; ++k) v[i][k] += f[k];
+            }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[i][k] *= rstd2 * w[k];
-        Raw<T, kVec>::st(p.y, row * p.dim + c, v[i]);
-    }
+            for (int k = 0; k < kVec; ++k) sum2[0] = fmaf(v[i][k], v[i][k], sum2[0]);
+            if (p.out) Raw<TR, kVec>::st(p.out, row * p.dim + c, v[i]);
+        }
+        if (kRing) {
+            const long long next = base + gridDim.x, later = base + (long long)p.stages * gridDim.x;
+            const int was = stage;
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            first[0] = 0.f;
+            if (next < p.rows) {
+                if (!mbar_wait(&full[stage], phase, &kNoAbortRow, kRowWaitNs)) failed[odd] = 1;
+                if (p.weight)
+                    first[0] = stage_sum<T, kVec, kNV>(p, dyn + (size_t)stage * p.stage_bytes,
+                                                       grp < p.groups, grp, lane, m.tg, gs);
+            }
+            sum_row_and_group(sum2[0], first[0], m, first_g, red[0]);
+            if (*(volatile int *)&failed[odd]) {
+                row_copy_failed(p, full, stage, phase, next, p.stages - 1);
+                return;
+            }
+            if (t == 0 && later < p.rows) fetch_row<T, TR>(p, at, &full[was], later, false);
+            odd ^= 1;
+        }
+        if (!p.next_weight) continue;
+        if (!kRing) sum_over(sum2, m.row_threads, first_r, red[1]);
+        const float rstd2 = rsqrtf(sum2[0] * inv_dim + p.eps);
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int e = (i * m.tg + lane) * kVec;
+            if (!live || e >= gs) continue;
+            const int c = grp * gs + e;
+            float w[kVec];
+            ld_weight<kVec>(p.next_weight, c, w);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[i][k] *= rstd2 * w[k];
+            Raw<T, kVec>::st(p.y, row * p.dim + c, v[i]);
+        }
     }
 }
 

@@ -442,246 +442,246 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     // could be two phases on by then.
     constexpr int kUBufs = C::UBufs, kVBufs = C::VpBufs;
     if (warp < 4) {
-    if (warp == kWarpTma) {
-        // ---- producer: tiles by TMA, decays by the warp -----------------------------
-        const CUtensorMap *mq = &maps.m[a.map[0]], *mk = &maps.m[a.map[1]],
-                          *mv = &maps.m[a.map[2]], *md = &maps.m[a.map[3]];
-        const int hq = h / a.q_group, hk = h / a.k_group, hv = h / a.v_group,
-                  hd = has_dot ? h / a.dot_group : 0;
-        const float gh = p.g ? 0.f : p.g_head ? __ldg(p.g_head + h) : 0.f;
-        auto raw = [&](int i, int e) -> float {  // the log decay of token 2·lane + e of chunk i
-            const int tok = chunk_of(i) * kC + 2 * lane + e;
-            if (i >= n || tok >= len) return 0.f;
-            return p.g ? ldg_f32(static_cast<const bf16 *>(p.g) +
-                                 ((long long)b * p.seqlen + tok) * p.heads + h)
-                       : gh;
-        };
-        float r0 = raw(0, 0), r1 = raw(0, 1);
-        double seg_log2 = 0.0;
-        int issued = 0;
-        for (int i = 0; i < n; ++i) {
-            const int s = i % kStages;
-            ok = wait(&S.empty[s], ((i / kStages) & 1) ^ 1);
-            if (!ok) break;
-            const int t0 = chunk_of(i) * kC;
-            if (lane == 0) {
-                constexpr int kSlabs = D / 64;
-                constexpr uint32_t kBytes = kSlabs * kC * 128;
-                mbar_arrive_expect_tx(&S.full[s],
-                                      kBytes * (kFull ? (has_dot ? 4 : 3) : 2));
+        if (warp == kWarpTma) {
+            // ---- producer: tiles by TMA, decays by the warp -----------------------------
+            const CUtensorMap *mq = &maps.m[a.map[0]], *mk = &maps.m[a.map[1]],
+                              *mv = &maps.m[a.map[2]], *md = &maps.m[a.map[3]];
+            const int hq = h / a.q_group, hk = h / a.k_group, hv = h / a.v_group,
+                      hd = has_dot ? h / a.dot_group : 0;
+            const float gh = p.g ? 0.f : p.g_head ? __ldg(p.g_head + h) : 0.f;
+            auto raw = [&](int i, int e) -> float {  // the log decay of token 2·lane + e of chunk i
+                const int tok = chunk_of(i) * kC + 2 * lane + e;
+                if (i >= n || tok >= len) return 0.f;
+                return p.g ? ldg_f32(static_cast<const bf16 *>(p.g) +
+                                     ((long long)b * p.seqlen + tok) * p.heads + h)
+                           : gh;
+            };
+            float r0 = raw(0, 0), r1 = raw(0, 1);
+            double seg_log2 = 0.0;
+            int issued = 0;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % kStages;
+                ok = wait(&S.empty[s], ((i / kStages) & 1) ^ 1);
+                if (!ok) break;
+                const int t0 = chunk_of(i) * kC;
+                if (lane == 0) {
+                    constexpr int kSlabs = D / 64;
+                    constexpr uint32_t kBytes = kSlabs * kC * 128;
+                    mbar_arrive_expect_tx(&S.full[s],
+                                          kBytes * (kFull ? (has_dot ? 4 : 3) : 2));
 #pragma unroll
-                for (int sl = 0; sl < kSlabs; ++sl) {
-                    if (kFull)
-                        tma_load_4d(&S.tile[s][0][sl * kC * 64], mq, &S.full[s], sl * 64, hq, t0, b);
-                    tma_load_4d(&S.tile[s][Smem::kK][sl * kC * 64], mk, &S.full[s], sl * 64, hk, t0,
-                                b);
-                    tma_load_4d(&S.tile[s][Smem::kV][sl * kC * 64], mv, &S.full[s], sl * 64, hv, t0,
-                                b);
-                    if (has_dot)
-                        tma_load_4d(&S.tile[s][Smem::kTiles - 1][sl * kC * 64], md, &S.full[s],
-                                    sl * 64, hd, t0, b);
+                    for (int sl = 0; sl < kSlabs; ++sl) {
+                        if (kFull)
+                            tma_load_4d(&S.tile[s][0][sl * kC * 64], mq, &S.full[s], sl * 64, hq, t0, b);
+                        tma_load_4d(&S.tile[s][Smem::kK][sl * kC * 64], mk, &S.full[s], sl * 64, hk, t0,
+                                    b);
+                        tma_load_4d(&S.tile[s][Smem::kV][sl * kC * 64], mv, &S.full[s], sl * 64, hv, t0,
+                                    b);
+                        if (has_dot)
+                            tma_load_4d(&S.tile[s][Smem::kTiles - 1][sl * kC * 64], md, &S.full[s],
+                                        sl * 64, hd, t0, b);
+                    }
                 }
-            }
-            issued = i + 1;
-            double g0 = (double)r0 * 1.4426950408889634, g1 = (double)r1 * 1.4426950408889634;
-            r0 = raw(i + 1, 0);
-            r1 = raw(i + 1, 1);
-            g0 = g0 < kLaResetLog2 ? kLaResetLog2 : g0;
-            g1 = g1 < kLaResetLog2 ? kLaResetLog2 : g1;
-            double sum = g0 + g1;
+                issued = i + 1;
+                double g0 = (double)r0 * 1.4426950408889634, g1 = (double)r1 * 1.4426950408889634;
+                r0 = raw(i + 1, 0);
+                r1 = raw(i + 1, 1);
+                g0 = g0 < kLaResetLog2 ? kLaResetLog2 : g0;
+                g1 = g1 < kLaResetLog2 ? kLaResetLog2 : g1;
+                double sum = g0 + g1;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, sum, m);
-                if (lane >= m) sum += o;
-            }
-            const double end = __shfl_sync(0xffffffffu, sum, 31);
-            // A: the log2 of what separates a token from the state entering (in the sweep's
-            // direction); a pair's weight is 2^(A_row − A_col)
-            const double G[2] = {sum - g1, sum};
-            float A[2], row[2], colf[2], colw[2];
-            bool far = false;
+                for (int m = 1; m < 32; m <<= 1) {
+                    const double o = __shfl_up_sync(0xffffffffu, sum, m);
+                    if (lane >= m) sum += o;
+                }
+                const double end = __shfl_sync(0xffffffffu, sum, 31);
+                // A: the log2 of what separates a token from the state entering (in the sweep's
+                // direction); a pair's weight is 2^(A_row − A_col)
+                const double G[2] = {sum - g1, sum};
+                float A[2], row[2], colf[2], colw[2];
+                bool far = false;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                A[e] = (float)(rev ? end - G[e] : G[e]);
-                far = far || !(fabsf(A[e]) <= kRange);
-                row[e] = a.row_scale * ex2_approx(A[e]);
-                colf[e] = a.col_scale * ex2_approx(-A[e]);
-                colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
+                for (int e = 0; e < 2; ++e) {
+                    A[e] = (float)(rev ? end - G[e] : G[e]);
+                    far = far || !(fabsf(A[e]) <= kRange);
+                    row[e] = a.row_scale * ex2_approx(A[e]);
+                    colf[e] = a.col_scale * ex2_approx(-A[e]);
+                    colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
+                }
+                far = __any_sync(0xffffffffu, far);
+                const int sl = i % kSlots;
+                *reinterpret_cast<float2 *>(&S.A[sl][2 * lane]) = make_float2(A[0], A[1]);
+                *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) = make_float2(row[0], row[1]);
+                *reinterpret_cast<float2 *>(&S.colf[sl][2 * lane]) = make_float2(colf[0], colf[1]);
+                *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) = make_float2(colw[0], colw[1]);
+                if (lane == 0) {
+                    S.decay[sl] = ex2_approx((float)end);
+                    S.strong[sl] = far;
+                }
+                seg_log2 += end;
+                arrive(&S.full[s]);
+                if (lane == 0) mbar_arrive(&S.factors[sl]);
             }
-            far = __any_sync(0xffffffffu, far);
-            const int sl = i % kSlots;
-            *reinterpret_cast<float2 *>(&S.A[sl][2 * lane]) = make_float2(A[0], A[1]);
-            *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) = make_float2(row[0], row[1]);
-            *reinterpret_cast<float2 *>(&S.colf[sl][2 * lane]) = make_float2(colf[0], colf[1]);
-            *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) = make_float2(colw[0], colw[1]);
-            if (lane == 0) {
-                S.decay[sl] = ex2_approx((float)end);
-                S.strong[sl] = far;
+            if (!kFull && lane == 0)
+                a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
+            if (!ok) {  // copies still in flight land before the block goes
+                const int none = 0;
+                for (int i = max(0, issued - kStages); i < issued; ++i)
+                    wait_bar(&S.full[i % kStages], (i / kStages) & 1, &none);
             }
-            seg_log2 += end;
-            arrive(&S.full[s]);
-            if (lane == 0) mbar_arrive(&S.factors[sl]);
-        }
-        if (!kFull && lane == 0)
-            a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
-        if (!ok) {  // copies still in flight land before the block goes
-            const int none = 0;
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                wait_bar(&S.full[i % kStages], (i / kStages) & 1, &none);
-        }
-    } else if (warp == kWarpMma) {
-        // ---- MMA issuer ---------------------------------------------------------------
-        // The warp waits (a lane per barrier, so that several waits cost one), an elected
-        // lane issues. Descriptors are a tile's first plus an offset in 16-byte units:
-        // an MMA of 64 columns is bound by its issue (about 50 clocks).
-        constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
-        constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
-        constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
-        constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
-        constexpr uint32_t kSlab = kC * 128;
-        auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2,
-                         uint32_t p2) -> bool {
-            bool done = true;
-            if (lane < 3)
-                done = wait_bar(lane == 0 ? b0 : lane == 1 ? b1 : b2,
-                                (lane == 0 ? p0 : lane == 1 ? p1 : p2) & 1, &S.abort);
-            ok = __all_sync(0xffffffffu, done);
-            tc_fence_after();
-            return ok;
-        };
-        auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) -> bool {
-            return wait3(b0, p0, b1, p1, b1, p1);
-        };
-        // K-major: steps of 16 columns inside slabs of 64; M- or N-major: steps of 16
-        // tokens, two 8-row atoms
-        auto kstep = [](int x) { return (uint64_t)(((x >> 2) * kSlab + (x & 3) * 32) >> 4); };
-        constexpr uint64_t kTok = 2048 >> 4;
-        auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
-            const int s = i % kStages;
-            const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024),
-                           k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), 16, 1024);
-            if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
-            if (elect_one()) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                    umma_bf16(tmem + C::S, q + kstep(x), k + kstep(x), id_s, x > 0);
-                umma_commit(&S.s_full);
-            }
-            __syncwarp();
-        };
-        if (kFull && n > 0) scores(0);
-        for (int i = 0; ok && i < n; ++i) {
-            const int s = i % kStages;
-            const uint64_t k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), kSlab, 1024);
-            const int ub = i % kUBufs, vb = i % kVBufs;
-            // U: both operands' K is the token. Its tiles have landed: c ◦ V was made from them.
-            if (!wait2(&S.vp_full[vb], i / kVBufs, &S.u_empty[ub], ((i / kUBufs) & 1) ^ 1)) break;
-            if (elect_one()) {
-                const uint32_t u = tmem + C::U + ub * D;
-#pragma unroll
-                for (int part = 0; part < (int)C::VpParts; ++part)
-#pragma unroll
-                    for (int x = 0; x < kC / 16; ++x)
-                        umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok, id_u,
-                                     part > 0 || x > 0);
-                umma_commit(&S.u_full[ub]);
-                if (kVBufs != kUBufs) umma_commit(&S.vp_empty[vb]);
-                if (!kFull) umma_commit(&S.empty[s]);
-            }
-            __syncwarp();
-            if (!kFull) continue;
-            if (i + 1 < n) scores(i + 1);
-            // Ye = S_inᵀ Qᵀ and Yi = Vᵀ Pᵀ, the second on top of the first where the row
-            // factors stand in the outputs
-            const bool two = kBwd || S.strong[i % kSlots] != 0;
-            const uint32_t yi = tmem + C::Yi, ye = two ? tmem + C::Ye : yi;
-            const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024);
-            const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
-                           pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
-            if (!ok || !wait3(&S.o_empty, (i & 1) ^ 1, &S.st_full, i, &S.p_full, i)) break;
-            // U reads c ◦ V from where this Ye goes
-            if (C::VpOnYe && two && vb && !wait2(&S.vp_empty[vb], i / kVBufs, &S.p_full, i)) break;
-            if (elect_one()) {
-#pragma unroll
-                for (int part = 0; part < (int)C::StParts; ++part)
+        } else if (warp == kWarpMma) {
+            // ---- MMA issuer ---------------------------------------------------------------
+            // The warp waits (a lane per barrier, so that several waits cost one), an elected
+            // lane issues. Descriptors are a tile's first plus an offset in 16-byte units:
+            // an MMA of 64 columns is bound by its issue (about 50 clocks).
+            constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
+            constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
+            constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
+            constexpr uint32_t id_u = idesc_bf16(128, D, 0, 1);    // c ◦ V (tensor memory), K (N-major)
+            constexpr uint32_t kSlab = kC * 128;
+            auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2,
+                             uint32_t p2) -> bool {
+                bool done = true;
+                if (lane < 3)
+                    done = wait_bar(lane == 0 ? b0 : lane == 1 ? b1 : b2,
+                                    (lane == 0 ? p0 : lane == 1 ? p1 : p2) & 1, &S.abort);
+                ok = __all_sync(0xffffffffu, done);
+                tc_fence_after();
+                return ok;
+            };
+            auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) -> bool {
+                return wait3(b0, p0, b1, p1, b1, p1);
+            };
+            // K-major: steps of 16 columns inside slabs of 64; M- or N-major: steps of 16
+            // tokens, two 8-row atoms
+            auto kstep = [](int x) { return (uint64_t)(((x >> 2) * kSlab + (x & 3) * 32) >> 4); };
+            constexpr uint64_t kTok = 2048 >> 4;
+            auto scores = [&](int i) {  // rows 64 .. 127 of A are whatever follows the tile
+                const int s = i % kStages;
+                const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024),
+                               k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), 16, 1024);
+                if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
+                if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x)
-                        umma_bf16_ts(ye, tmem + C::St + part * (D / 2) + x * 8, q + kstep(x), id_ye,
-                                     part > 0 || x > 0);
-                umma_commit(&S.st_empty);
-#pragma unroll
-                for (int x = 0; x < kC / 16; ++x)
-                    umma_bf16(yi, v + x * kTok, pp + kstep(x), id_yi, !two || x > 0);
-                umma_commit(&S.o_full);
-                umma_commit(&S.p_empty);
-                umma_commit(&S.empty[s]);
-            }
-            __syncwarp();
-        }
-        if (!ok) {  // MMAs in flight end before tensor memory is given back
-            const int none = 0;
-            if (elect_one()) {
-                umma_commit(&S.drain);
-                wait_bar(&S.drain, 0, &none);
-            }
-            __syncwarp();
-        }
-    } else {
-        // ---- P: weights of the products inside the chunk, a row per lane ---------------
-        if (kFull) {
-            const int r = 32 * warp + lane;
-            for (int i = 0; i < n; ++i) {
-                const int nq = min(kC, len - chunk_of(i) * kC), sl = i % kSlots;
-                ok = wait(&S.factors[sl], i / kSlots) && wait(&S.s_full, i);
-                if (!ok) break;
-                tc_fence_after();
-                const bool strong = S.strong[sl] != 0;
-                const float rf = S.rowf[sl][r], ar = S.A[sl][r], both = a.row_scale * a.col_scale;
-                const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
-                char *row = reinterpret_cast<char *>(S.P) + r * 128;
-                uint32_t out[16];
-                auto block = [&](int half, bool last) {
-                    float v[32];
-                    tmem_ld32(tmem + lanes + C::S + 32 * half, v);
-                    if (last) {
-                        tc_fence_before();
-                        arrive(&S.s_empty);  // the next chunk's scores may come
-                    }
-                    if (strong)
-                        score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar, lo - 32 * half,
-                                                  hi - 32 * half, out);
-                    else
-                        score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
-                                                   lo - 32 * half, hi - 32 * half, out);
-                };
-                // the block off the diagonal (of the warp that has one, else zeros), then
-                // the one on it
-                const bool off = warp == (rev ? 0 : 1);
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    const int half = k ? warp : 1 - warp;
-                    if (k || off) {
-                        block(half, k == 1);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) out[e] = 0;
-                    }
-                    if (k == 0) {
-                        ok = wait(&S.p_empty, (i & 1) ^ 1);
-                        if (!ok) break;
-                    }
-#pragma unroll
-                    for (int c8 = 0; c8 < 4; ++c8)
-                        *reinterpret_cast<uint4 *>(row + (((4 * half + c8) ^ (r & 7)) << 4)) =
-                            make_uint4(out[4 * c8], out[4 * c8 + 1], out[4 * c8 + 2],
-                                       out[4 * c8 + 3]);
+                        umma_bf16(tmem + C::S, q + kstep(x), k + kstep(x), id_s, x > 0);
+                    umma_commit(&S.s_full);
                 }
-                if (!ok) break;
-                fence_proxy_async_smem();
-                arrive(&S.p_full);
+                __syncwarp();
+            };
+            if (kFull && n > 0) scores(0);
+            for (int i = 0; ok && i < n; ++i) {
+                const int s = i % kStages;
+                const uint64_t k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), kSlab, 1024);
+                const int ub = i % kUBufs, vb = i % kVBufs;
+                // U: both operands' K is the token. Its tiles have landed: c ◦ V was made from them.
+                if (!wait2(&S.vp_full[vb], i / kVBufs, &S.u_empty[ub], ((i / kUBufs) & 1) ^ 1)) break;
+                if (elect_one()) {
+                    const uint32_t u = tmem + C::U + ub * D;
+#pragma unroll
+                    for (int part = 0; part < (int)C::VpParts; ++part)
+#pragma unroll
+                        for (int x = 0; x < kC / 16; ++x)
+                            umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok, id_u,
+                                         part > 0 || x > 0);
+                    umma_commit(&S.u_full[ub]);
+                    if (kVBufs != kUBufs) umma_commit(&S.vp_empty[vb]);
+                    if (!kFull) umma_commit(&S.empty[s]);
+                }
+                __syncwarp();
+                if (!kFull) continue;
+                if (i + 1 < n) scores(i + 1);
+                // Ye = S_inᵀ Qᵀ and Yi = Vᵀ Pᵀ, the second on top of the first where the row
+                // factors stand in the outputs
+                const bool two = kBwd || S.strong[i % kSlots] != 0;
+                const uint32_t yi = tmem + C::Yi, ye = two ? tmem + C::Ye : yi;
+                const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024);
+                const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
+                               pp = umma_desc_sw128(smem_addr(S.P), 16, 1024);
+                if (!ok || !wait3(&S.o_empty, (i & 1) ^ 1, &S.st_full, i, &S.p_full, i)) break;
+                // U reads c ◦ V from where this Ye goes
+                if (C::VpOnYe && two && vb && !wait2(&S.vp_empty[vb], i / kVBufs, &S.p_full, i)) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int part = 0; part < (int)C::StParts; ++part)
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x)
+                            umma_bf16_ts(ye, tmem + C::St + part * (D / 2) + x * 8, q + kstep(x), id_ye,
+                                         part > 0 || x > 0);
+                    umma_commit(&S.st_empty);
+#pragma unroll
+                    for (int x = 0; x < kC / 16; ++x)
+                        umma_bf16(yi, v + x * kTok, pp + kstep(x), id_yi, !two || x > 0);
+                    umma_commit(&S.o_full);
+                    umma_commit(&S.p_empty);
+                    umma_commit(&S.empty[s]);
+                }
+                __syncwarp();
+            }
+            if (!ok) {  // MMAs in flight end before tensor memory is given back
+                const int none = 0;
+                if (elect_one()) {
+                    umma_commit(&S.drain);
+                    wait_bar(&S.drain, 0, &none);
+                }
+                __syncwarp();
+            }
+        } else {
+            // ---- P: weights of the products inside the chunk, a row per lane ---------------
+            if (kFull) {
+                const int r = 32 * warp + lane;
+                for (int i = 0; i < n; ++i) {
+                    const int nq = min(kC, len - chunk_of(i) * kC), sl = i % kSlots;
+                    ok = wait(&S.factors[sl], i / kSlots) && wait(&S.s_full, i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const bool strong = S.strong[sl] != 0;
+                    const float rf = S.rowf[sl][r], ar = S.A[sl][r], both = a.row_scale * a.col_scale;
+                    const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
+                    char *row = reinterpret_cast<char *>(S.P) + r * 128;
+                    uint32_t out[16];
+                    auto block = [&](int half, bool last) {
+                        float v[32];
+                        tmem_ld32(tmem + lanes + C::S + 32 * half, v);
+                        if (last) {
+                            tc_fence_before();
+                            arrive(&S.s_empty);  // the next chunk's scores may come
+                        }
+                        if (strong)
+                            score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar, lo - 32 * half,
+                                                      hi - 32 * half, out);
+                        else
+                            score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
+                                                       lo - 32 * half, hi - 32 * half, out);
+                    };
+                    // the block off the diagonal (of the warp that has one, else zeros), then
+                    // the one on it
+                    const bool off = warp == (rev ? 0 : 1);
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        const int half = k ? warp : 1 - warp;
+                        if (k || off) {
+                            block(half, k == 1);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) out[e] = 0;
+                        }
+                        if (k == 0) {
+                            ok = wait(&S.p_empty, (i & 1) ^ 1);
+                            if (!ok) break;
+                        }
+#pragma unroll
+                        for (int c8 = 0; c8 < 4; ++c8)
+                            *reinterpret_cast<uint4 *>(row + (((4 * half + c8) ^ (r & 7)) << 4)) =
+                                make_uint4(out[4 * c8], out[4 * c8 + 1], out[4 * c8 + 2],
+                                           out[4 * c8 + 3]);
+                    }
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    arrive(&S.p_full);
+                }
             }
         }
-    }
     } else if (warp < 8 || (!kFull && warp >= 16)) {
         // ---- c ◦ V as bfloat16 parts, column d of V on lane d --------------------------
         // In the pass over the segments' own states the output warps take every other chunk.
@@ -858,93 +858,93 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         }
     } else {
         if (kFull) {
-        // ---- outputs: lane d, a column per token -----------------------------------------
-        const int d0 = 32 * (warp & 3);
-        const int tl = t - 512;  // 0 .. 127
-        const CUtensorMap *my = &maps.m[a.map_y];
-        const bool f32 = kBwd && a.y_f32;
-        uint32_t syncs = 0;
-        int strongs = 0;
-        for (int i = 0; i < n; ++i) {
-            const int s = i % kStages;
-            const int t0 = chunk_of(i) * kC, nq = min(kC, len - t0);
-            ok = wait(&S.factors[i % kSlots], i / kSlots) && wait(&S.o_full, i);
-            if (!ok) break;
-            tc_fence_after();
-            if (tl == 0) bulk_wait_read<0>();  // the previous chunk's store has read the staging
-            arrive(&S.o_sync);
-            ok = wait(&S.o_sync, syncs++);
-            if (!ok) break;
-            if (d0 < D) {
-                // float32 rows (the heads' parts of a shared gradient) go straight to memory
-                const int nl = (int)min((long long)kC, p.seqlen - t0);
-                const long long y_row = (long long)p.heads * a.dv;
-                float *yf = f32 ? static_cast<float *>(a.y) +
-                                      ((long long)b * p.seqlen + t0) * y_row + h * a.dv
-                                : nullptr;
-                const bf16 *dot = S.tile[s][Smem::kTiles - 1];
-                const uint32_t t_y = tmem + lanes + C::Yi, t_ye = tmem + lanes + C::Ye;
-                auto done = [&]() {  // the next chunk's products may come
-                    tc_fence_before();
-                    arrive(&S.o_empty);
-                    if (C::VpOnYe && S.strong[i % kSlots]) arrive(&S.ye_read[strongs++ & 3]);
-                };
-                auto rows = [&](auto is_f32, auto is_dot) {
-                    constexpr bool kF32 = decltype(is_f32)::value, kDot = decltype(is_dot)::value;
-                    const int sl = i % kSlots;
-                    if (S.strong[sl])
-                        output_rows<kF32, kDot, true, true>(t_y, t_ye, S.out, dot, S.red[warp & 3],
-                                                            S.rowf[sl], d0, yf, y_row, nl, a.dv,
-                                                            done);
-                    else
-                        output_rows<kF32, kDot, kBwd, false>(t_y, t_ye, S.out, dot,
-                                                             S.red[warp & 3], S.rowf[sl], d0, yf,
-                                                             y_row, nl, a.dv, done);
-                };
-                if constexpr (kBwd) {
-                    if (has_dot && f32)
-                        rows(Yes(), Yes());
-                    else if (has_dot)
-                        rows(No(), Yes());
-                    else if (f32)
-                        rows(Yes(), No());
-                    else
+            // ---- outputs: lane d, a column per token -----------------------------------------
+            const int d0 = 32 * (warp & 3);
+            const int tl = t - 512;  // 0 .. 127
+            const CUtensorMap *my = &maps.m[a.map_y];
+            const bool f32 = kBwd && a.y_f32;
+            uint32_t syncs = 0;
+            int strongs = 0;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % kStages;
+                const int t0 = chunk_of(i) * kC, nq = min(kC, len - t0);
+                ok = wait(&S.factors[i % kSlots], i / kSlots) && wait(&S.o_full, i);
+                if (!ok) break;
+                tc_fence_after();
+                if (tl == 0) bulk_wait_read<0>();  // the previous chunk's store has read the staging
+                arrive(&S.o_sync);
+                ok = wait(&S.o_sync, syncs++);
+                if (!ok) break;
+                if (d0 < D) {
+                    // float32 rows (the heads' parts of a shared gradient) go straight to memory
+                    const int nl = (int)min((long long)kC, p.seqlen - t0);
+                    const long long y_row = (long long)p.heads * a.dv;
+                    float *yf = f32 ? static_cast<float *>(a.y) +
+                                          ((long long)b * p.seqlen + t0) * y_row + h * a.dv
+                                    : nullptr;
+                    const bf16 *dot = S.tile[s][Smem::kTiles - 1];
+                    const uint32_t t_y = tmem + lanes + C::Yi, t_ye = tmem + lanes + C::Ye;
+                    auto done = [&]() {  // the next chunk's products may come
+                        tc_fence_before();
+                        arrive(&S.o_empty);
+                        if (C::VpOnYe && S.strong[i % kSlots]) arrive(&S.ye_read[strongs++ & 3]);
+                    };
+                    auto rows = [&](auto is_f32, auto is_dot) {
+                        constexpr bool kF32 = decltype(is_f32)::value, kDot = decltype(is_dot)::value;
+                        const int sl = i % kSlots;
+                        if (S.strong[sl])
+                            output_rows<kF32, kDot, true, true>(t_y, t_ye, S.out, dot, S.red[warp & 3],
+                                                                S.rowf[sl], d0, yf, y_row, nl, a.dv,
+                                                                done);
+                        else
+                            output_rows<kF32, kDot, kBwd, false>(t_y, t_ye, S.out, dot,
+                                                                 S.red[warp & 3], S.rowf[sl], d0, yf,
+                                                                 y_row, nl, a.dv, done);
+                    };
+                    if constexpr (kBwd) {
+                        if (has_dot && f32)
+                            rows(Yes(), Yes());
+                        else if (has_dot)
+                            rows(No(), Yes());
+                        else if (f32)
+                            rows(Yes(), No());
+                        else
+                            rows(No(), No());
+                    } else {
                         rows(No(), No());
+                    }
                 } else {
-                    rows(No(), No());
+                    arrive(&S.o_empty);
                 }
-            } else {
-                arrive(&S.o_empty);
-            }
-            if (has_dot) arrive(&S.empty[s]);
-            fence_proxy_async_smem();
-            arrive(&S.o_sync);
-            ok = wait(&S.o_sync, syncs++);
-            if (!ok) break;
-            if (tl == 0 && !f32) {
-                for (int c = 0; c < a.dv; c += 64)
-                    tma_store_4d(my, S.out + (c >> 6) * (kC * 64), c, h, t0, b);
-                bulk_commit();
-            }
-            if (kBwd && has_dot && tl < nq) {
-                float sum = 0.f;
+                if (has_dot) arrive(&S.empty[s]);
+                fence_proxy_async_smem();
+                arrive(&S.o_sync);
+                ok = wait(&S.o_sync, syncs++);
+                if (!ok) break;
+                if (tl == 0 && !f32) {
+                    for (int c = 0; c < a.dv; c += 64)
+                        tma_store_4d(my, S.out + (c >> 6) * (kC * 64), c, h, t0, b);
+                    bulk_commit();
+                }
+                if (kBwd && has_dot && tl < nq) {
+                    float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) sum += S.red[w][tl];
-                a.dot_out[bh * p.seqlen + t0 + tl] = sum;
+                    for (int w = 0; w < D / 32; ++w) sum += S.red[w][tl];
+                    a.dot_out[bh * p.seqlen + t0 + tl] = sum;
+                }
             }
-        }
-        if (tl == 0) bulk_wait<0>();  // the last stores are out before the block ends
-        // chunks without a token: zeros
-        const long long row0 = (long long)b * p.seqlen;
-        for (long long tok = (long long)c_live * kC; tok < min((long long)c_end * kC, p.seqlen);
-             ++tok) {
-            const long long off = ((row0 + tok) * p.heads + h) * a.dv + tl;
-            if (tl >= a.dv) break;
-            if (f32)
-                static_cast<float *>(a.y)[off] = 0.f;
-            else
-                static_cast<bf16 *>(a.y)[off] = __float2bfloat16_rn(0.f);
-        }
+            if (tl == 0) bulk_wait<0>();  // the last stores are out before the block ends
+            // chunks without a token: zeros
+            const long long row0 = (long long)b * p.seqlen;
+            for (long long tok = (long long)c_live * kC; tok < min((long long)c_end * kC, p.seqlen);
+                 ++tok) {
+                const long long off = ((row0 + tok) * p.heads + h) * a.dv + tl;
+                if (tl >= a.dv) break;
+                if (f32)
+                    static_cast<float *>(a.y)[off] = 0.f;
+                else
+                    static_cast<bf16 *>(a.y)[off] = __float2bfloat16_rn(0.f);
+            }
         }
     }
 

@@ -51,7 +51,7 @@ int check_dims(const LaDims &d, int dtype) {
 // tc: the tensor-core kernels.
 LinattnPlan plan_for(const LaDims &d, int nsweeps, bool tc) {
     const int64_t ctas = d.pairs() * nsweeps;
-    if (tc) return linattn_plan(d.seqlen, ctas, sm_count(), 3.0, 0.6);
+    if (tc) return linattn_plan(d.seqlen, ctas, sm_count(), 3.0, 0.55);
     return linattn_plan(d.seqlen, ctas * linattn_tiles((int)std::max(d.dk, d.dv)),
                         sm_count() * linattn_slots((int)d.dk, (int)d.dv), 0.5, 0.5);
 }
@@ -154,6 +154,7 @@ LinattnParams base_params(const LaDims &d, const LaInputs &in, const LinattnPlan
     p.heads = (int)d.heads;
     p.nchunks = pl.nchunks;
     p.nseg = pl.nseg;
+    p.first_chunks = pl.first_chunks;
     p.seg_chunks = pl.seg_chunks;
     return p;
 }

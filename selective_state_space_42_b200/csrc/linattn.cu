@@ -166,18 +166,21 @@ template <typename T, int DKP, bool kFull>
 __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_constant__ LinattnParams p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SweepSmem<DKP> &S = *reinterpret_cast<SweepSmem<DKP> *>(smem_raw);
-    const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
     constexpr int kTiles = DKP / kVt;
     long long id = blockIdx.x;
     const int tile = (int)(id % kTiles);
     id /= kTiles;
-    const int order = (int)(id % nruns);  // position in the sweep's direction
-    id /= nruns;
+    const int order = p.order0 + (int)(id % p.orders);  // position in the sweep's direction
+    id /= p.orders;
     const int sw = (int)(id % p.nsweeps);
     const long long bh = id / p.nsweeps;
     const SweepArgs &a = p.sweep[sw];
     const int v0 = tile * kVt;
-    if (v0 >= a.dv) return;
+    if (kFull && p.nseg > 1 && order == 0) linattn_let_states_start();
+    if (v0 >= a.dv) {
+        if (!kFull && blockIdx.x == gridDim.x - 1) linattn_wait_for_first();
+        return;
+    }
     const long long b = bh / p.heads;
     const int h = (int)(bh % p.heads);
     const int seg = a.reverse ? p.nseg - 1 - order : order;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
             for (int c = 0; c < 4; ++c) {
                 const int v = v0 + 4 * tx + c;
                 if (v >= a.dv) continue;
-                if (p.nseg > 1)
+                if (order > 0)
                     e[c] = a.seg_state[(bh * p.nseg + seg) * state_elems + (long long)d * a.dv + v];
                 else if (a.h_init)
                     e[c] = a.h_init[bh * state_elems + (a.h_init_t ? (long long)v * a.dk + d
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
     }
     double seg_log2 = 0.0;  // of the segment's decay (thread 0)
 
-    const int c_first = seg * p.seg_chunks;
-    const int c_last = min(p.nchunks, c_first + p.seg_chunks);
+    int c_first, c_last;
+    linattn_segment(p, a.reverse != 0, order, &c_first, &c_last);
     for (int i = 0; i < c_last - c_first; ++i) {
         const int c = a.reverse ? c_last - 1 - i : c_first + i;
         const long long t0 = (long long)c * kC;
@@ -383,9 +386,10 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
 
     float *out = nullptr;
     bool transposed = false;
-    if (!kFull) {
+    if (!kFull || (p.nseg > 1 && order == 0)) {
         out = a.seg_state + (bh * p.nseg + seg) * state_elems;
-        if (t == 0 && tile == 0) a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
+        if (t == 0 && tile == 0)
+            a.seg_decay[bh * p.nseg + seg] = kFull ? 0.f : ex2_approx((float)seg_log2);
     } else if (a.h_final && order == p.nseg - 1) {
         out = a.h_final + bh * state_elems;
         transposed = a.h_final_t != 0;
@@ -403,6 +407,7 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
             }
         }
     }
+    if (!kFull && blockIdx.x == gridDim.x - 1) linattn_wait_for_first();
 }
 
 // seg_state[s]: the segment's own state -> the state entering it, in the
@@ -562,15 +567,8 @@ cudaError_t launch_sweeps(const LinattnParams &p, cudaStream_t stream) {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const long long per_seg = p.batch * p.heads * p.nsweeps * (DKP / kVt);
-    if (p.nseg > 1) {
-        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem, stream>>>(p);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
-        if (e != cudaSuccess) return e;
-    }
-    full<<<(unsigned)(per_seg * p.nseg), kThr, smem, stream>>>(p);
-    return cudaGetLastError();
+    return linattn_launch(full, state, kThr, (int)smem, (int)smem,
+                          p.batch * p.heads * p.nsweeps * (DKP / kVt), p, stream);
 }
 
 }  // namespace
@@ -579,23 +577,25 @@ LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots, double hea
     LinattnPlan pl;
     pl.nchunks = (int)((seqlen + kLaChunk - 1) / kLaChunk);
     pl.nseg = 1;
-    pl.seg_chunks = pl.nchunks;
+    pl.first_chunks = pl.seg_chunks = pl.nchunks;
     // estimated time in chunk passes: waves of blocks × (start-up + chunks a
-    // segment); with several segments also the state pass, the carry and the
-    // two further launches
-    double best = (double)((ctas + slots - 1) / slots) * (head + pl.nchunks);
+    // segment); with several segments the first's and the states' kernels side by
+    // side, the others' full pass, the carry and the two further launches
+    auto waves = [&](long long blocks) { return (double)((blocks + slots - 1) / slots); };
+    double best = waves(ctas) * (head + pl.nchunks);
     const int most = ctas >= 8ll * slots ? 1 : pl.nchunks < 64 ? pl.nchunks : 64;
-    for (int n = 2; n <= most; ++n) {
-        const int per = (pl.nchunks + n - 1) / n;
-        const int segs = (pl.nchunks + per - 1) / per;
-        if (segs < 2) continue;
-        const double cost =
-            (double)((ctas * segs + slots - 1) / slots) * (head + per) +
-            (double)((ctas * (segs - 1) + slots - 1) / slots) * (head + own * per) + 6.0 +
-            0.05 * segs;
+    for (int n = 3; n <= most; ++n) {
+        const int per = (int)(pl.nchunks / (n - 1 + own)) + 1;
+        const int segs = 1 + (pl.nchunks - 1) / per;  // the first has what is left: 1 .. per
+        if (segs < 3) continue;
+        const int first = pl.nchunks - (segs - 1) * per;
+        const double both = waves(ctas * (segs - 1));
+        const double cost = both * (head + own * per) + std::max(0.0, first - own * per) +
+                            both * (head + per) + 6.0 + 0.05 * segs;
         if (cost < best) {
             best = cost;
             pl.nseg = segs;
+            pl.first_chunks = first;
             pl.seg_chunks = per;
         }
     }

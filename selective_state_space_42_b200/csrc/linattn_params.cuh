@@ -46,7 +46,8 @@ struct LinattnParams {
     const int *seqlens;           // [batch] or NULL
     long long batch, seqlen;
     int heads;
-    int nchunks, nseg, seg_chunks;
+    int nchunks, nseg, first_chunks, seg_chunks;
+    int order0, orders;           // the segments of a launch, in the sweep's order (set by it)
     int nsweeps;
     int vec;                      // every operand row allows 4-element vector loads
     int *status;                  // the library's device error word
@@ -57,12 +58,35 @@ struct LinattnParams {
 // and finite sums keep differences of resets well defined.
 constexpr double kLaResetLog2 = -160.0;
 
-// Plan: segments of a sequence that run side by side after a pass over their
-// own states. `ctas`: blocks of one segment; `slots`: blocks the device runs
-// at a time.
+// Plan: a sequence cut into segments. The first (in the sweep's order) runs whole
+// while a second kernel on the SMs left over finds the own states of the others but
+// the last; a carry turns these into the states entering, and the others run whole.
+// The first segment is the shorter one: its full pass takes as long as a state pass
+// over the others' seg_chunks. `ctas`: blocks of one segment; `slots`: blocks the
+// device runs at a time.
 struct LinattnPlan {
-    int nchunks, nseg, seg_chunks;
+    int nchunks, nseg, first_chunks, seg_chunks;
 };
+
+// Chunks [*first, *last) of a sweep's segment.
+__device__ __forceinline__ void linattn_segment(const LinattnParams &p, bool reverse, int order,
+                                                int *first, int *last) {
+    const int from = order ? p.first_chunks + (order - 1) * p.seg_chunks : 0;
+    const int to = min(p.nchunks, from + (order ? p.seg_chunks : p.first_chunks));
+    *first = reverse ? p.nchunks - to : from;
+    *last = reverse ? p.nchunks - from : to;
+}
+
+// The first segment's kernel, called at its start: the state kernel may take the SMs
+// that are left over.
+__device__ __forceinline__ void linattn_let_states_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// The state kernel, at its end: what follows waits for both kernels.
+__device__ __forceinline__ void linattn_wait_for_first() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // `head`: a block's start-up, `own`: the state pass's time, in chunk passes
 // and as a share of the full pass.
 LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots, double head, double own);
@@ -71,8 +95,40 @@ LinattnPlan linattn_plan(long long seqlen, long long ctas, int slots, double hea
 int linattn_tiles(int dv);  // 64-column tiles of a sweep (blocks per head and segment)
 int linattn_slots(int dk, int dv);
 cudaError_t launch_linattn_sweeps(const LinattnParams &p, bool bf16, cudaStream_t stream);
-// Carry: seg_state[s] becomes the state entering segment s.
+// Carry: seg_state[s] becomes the state entering segment s. A segment with decay
+// zero (the first, whose state has its initial one in it) is not added to.
 cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream);
+
+// The launches of a sweep: `full` and `state` take the arguments behind p, on
+// per_seg blocks a segment.
+template <typename Kernel, typename... Args>
+cudaError_t linattn_launch(Kernel full, Kernel state, int threads, int smem_full, int smem_state,
+                           long long per_seg, LinattnParams p, cudaStream_t stream,
+                           const Args &...args) {
+    p.order0 = 0;
+    p.orders = 1;
+    full<<<(unsigned)per_seg, threads, smem_full, stream>>>(p, args...);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.nseg == 1) return e;
+    p.order0 = 1;
+    p.orders = p.nseg - 2;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((unsigned)(per_seg * p.orders));
+    config.blockDim = dim3((unsigned)threads);
+    config.dynamicSmemBytes = (size_t)smem_state;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    e = cudaLaunchKernelEx(&config, state, p, args...);
+    if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
+    if (e != cudaSuccess) return e;
+    p.orders = p.nseg - 1;
+    full<<<(unsigned)(per_seg * p.orders), threads, smem_full, stream>>>(p, args...);
+    return cudaGetLastError();
+}
 
 // Tensor-core path (linattn_tc.cu): bfloat16 I/O, operands whose rows TMA can
 // read (16-byte rows and bases, dims multiples of 8); one block an SM.

@@ -376,9 +376,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     extern __shared__ __align__(128) unsigned char smem_raw[];
     // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
     Smem &S = *reinterpret_cast<Smem *>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
-    const int nruns = kFull ? p.nseg : p.nseg - 1;  // the last segment's own state is not needed
-    const int order = (int)(blockIdx.x % nruns);    // position in the sweep's direction
-    const long long id = blockIdx.x / nruns;
+    const int order = p.order0 + (int)(blockIdx.x % p.orders);  // in the sweep's direction
+    const long long id = blockIdx.x / p.orders;
+    if (kFull && p.nseg > 1 && order == 0) linattn_let_states_start();
     const SweepArgs &a = p.sweep[id % p.nsweeps];
     const long long bh = id / p.nsweeps;
     const int b = (int)(bh / p.heads), h = (int)(bh % p.heads);
@@ -386,7 +386,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     const int seg = rev ? p.nseg - 1 - order : order;
     const int len = p.seqlens ? (int)min((long long)max(__ldg(p.seqlens + b), 0), p.seqlen)
                               : (int)p.seqlen;
-    const int c_first = seg * p.seg_chunks, c_end = min(p.nchunks, c_first + p.seg_chunks);
+    int c_first, c_end;
+    linattn_segment(p, rev, order, &c_first, &c_end);
     const int c_live = max(c_first, min(c_end, (len + kC - 1) / kC));  // chunks with tokens
     const int n = c_live - c_first;
     auto chunk_of = [&](int i) { return rev ? c_live - 1 - i : c_first + i; };
@@ -522,8 +523,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 arrive(&S.full[s]);
                 if (lane == 0) mbar_arrive(&S.factors[sl]);
             }
-            if (!kFull && lane == 0)
-                a.seg_decay[bh * p.nseg + seg] = ex2_approx((float)seg_log2);
+            if ((!kFull || (p.nseg > 1 && order == 0)) && lane == 0)
+                a.seg_decay[bh * p.nseg + seg] = kFull ? 0.f : ex2_approx((float)seg_log2);
             if (!ok) {  // copies still in flight land before the block goes
                 const int none = 0;
                 for (int i = max(0, issued - kStages); i < issued; ++i)
@@ -783,7 +784,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         {
             const float *src = nullptr;
             bool tr = false;
-            if (kFull && p.nseg > 1) {
+            if (kFull && order > 0) {
                 src = a.seg_state + (bh * p.nseg + seg) * elems;
             } else if (kFull && a.h_init) {
                 src = a.h_init + bh * elems;
@@ -843,7 +844,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         }
         float *dst = nullptr;
         bool tr = false;
-        if (!kFull) {
+        if (!kFull || (p.nseg > 1 && order == 0)) {
             dst = a.seg_state + (bh * p.nseg + seg) * elems;
         } else if (a.h_final && order == p.nseg - 1) {
             dst = a.h_final + bh * elems;
@@ -958,6 +959,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpTma) tmem_dealloc(tmem, 512);
+    if (!kFull && blockIdx.x == gridDim.x - 1) linattn_wait_for_first();
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -987,15 +989,8 @@ cudaError_t launch(const LinattnParams &p, const TcMaps &maps, cudaStream_t stre
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_own);
     if (e != cudaSuccess) return e;
-    const long long per_seg = p.batch * p.heads * p.nsweeps;
-    if (p.nseg > 1) {
-        state<<<(unsigned)(per_seg * (p.nseg - 1)), kThr, smem_own, stream>>>(p, maps);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) e = launch_linattn_carry(p, stream);
-        if (e != cudaSuccess) return e;
-    }
-    full<<<(unsigned)(per_seg * p.nseg), kThr, smem, stream>>>(p, maps);
-    return cudaGetLastError();
+    return linattn_launch(full, state, kThr, smem, smem_own, p.batch * p.heads * p.nsweeps, p,
+                          stream, maps);
 }
 
 }  // namespace

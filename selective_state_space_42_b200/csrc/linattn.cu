@@ -15,12 +15,13 @@
 // A block carries the state of one head and 64 of its value columns through
 // the chunks of one segment, in registers (with a shared-memory copy for the
 // product with q). Too few heads to fill the device: the sequence is cut into
-// segments; a first pass finds each segment's own state, a carry over the
-// segments turns them into the states entering, and all segments run at once.
+// segments (LinattnPlan).
 //
 // Bound: the float32 FMA rate; per chunk 2·64·64·(dk + dv) + 2·2·64·dk·dv
 // operations a head, which the products' register tiles (4×4, and
-// (dk/16)×4 for the state) feed from shared memory.
+// (dk/16)×4 for the state) feed from shared memory. With few chunks a block, as on
+// 3 × 1111 tokens of 6 heads 48 → 80 in float32 (96–106 µs, 125 with equal segments
+// after a pass over all their states), the latency of a chunk: 19 µs.
 #include "linattn_params.cuh"
 
 #include <algorithm>

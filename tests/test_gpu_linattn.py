@@ -409,6 +409,31 @@ def test_shared_heads_and_ragged_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("given", ["h0", "dS", "neither"])
+def test_growing_states_and_one_state_given(dtype, given):
+    """Log decays of both signs, and a first state without a last one's gradient
+    and the other way round, over several segments."""
+    i = make(1, 1000, 1, 2, 64, 64, dtype, 30, h0=True)
+    i["g"] = (i["g"].float() * 0.25 * torch.tensor([1.0, -0.1])).to(DT[dtype])
+    for n in {"h0", "dS"} - {given}:
+        i[n] = None
+    check_fwd(i, dtype, what="growing")
+    check_bwd(i, dtype, what="growing")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_tensor_for_all_operands(dtype):
+    d = dev(make(1, 150, 2, 2, 64, 64, dtype, 31))
+    x = d["q"]
+    a = ss.selscan_linattn_bwd(x, x, x, d["g"], dy=x)
+    b = ss.selscan_linattn_bwd(x.clone(), x.clone(), x.clone(), d["g"], dy=x.clone())
+    assert torch.equal(ss.selscan_linattn_fwd(x, x, x, d["g"]),
+                       ss.selscan_linattn_fwd(x.clone(), x.clone(), x.clone(), d["g"]))
+    for n in ("dq", "dk", "dv", "dlog_decay"):
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_two_calls_at_once(dtype):
     """Calls on two streams at a time, each with its own workspace, give what
     they give one after the other."""

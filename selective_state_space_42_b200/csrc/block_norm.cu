@@ -16,7 +16,7 @@
 // group stay within its threads. All arithmetic and all sums are float32; the
 // only roundings to bfloat16 are the stores. 16384 rows of 5120 in bfloat16: 177 µs,
 // 73% of the HBM copy rate (the instructions' issue is at 75%); the gradient of 16384
-// rows of 2560, 321 µs, 45%: its column sums and operands take 96 registers a thread,
+// rows of 2560, 287 µs, 50%: its column sums and operands take 96 registers a thread,
 // which leaves 20 warps an SM to hide two barriers a row.
 #include "block_norm.cuh"
 #include "tma_util.cuh"
@@ -387,8 +387,10 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
 //   gate before: dgate = da·x, dx = da·silu(z)
 //   dz = dgate·silu'(z),  silu' = σ·(1 + z·(1 − σ))
 // Everything of the forward is recomputed from the inputs. Blocks stride over
-// the rows and keep the three column sums of their rows in registers; a
-// second kernel adds the blocks' sums in a fixed order.
+// the rows and keep the column sums of their rows in registers; a second kernel
+// adds the blocks' sums in a fixed order. Two sums do for three gradients: with
+// b = Σ dr·n (gate after: Σ dr·n·silu(z)), u = n·weight and dp = dr·res_scale (each
+// times the gate) make dres_scale = weight·b and dweight = res_scale·b.
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks, bool kRing>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
@@ -396,16 +398,16 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
     __shared__ uint64_t full[kMaxStages];
     __shared__ int failed[2];
     extern __shared__ __align__(128) unsigned char dyn[];
-    float *sums = reinterpret_cast<float *>(dyn);  // [3][dim] where a block has several rows
+    float *sums = reinterpret_cast<float *>(dyn);  // [2][dim] where a block has several rows
     const int t = threadIdx.x, local = t % m.row_threads;
     const int gs = p.dim / p.groups, grp = local / m.tg, lane = local % m.tg;
     const int sub = t / m.row_threads;
     const bool before = p.gate == kGateBefore, after = p.gate == kGateAfter;
-    float aw[kNV][kVec], as[kNV][kVec], an[kNV][kVec];
+    float ab[kNV][kVec], an[kNV][kVec];
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) aw[i][k] = as[i][k] = an[i][k] = 0.f;
+        for (int k = 0; k < kVec; ++k) ab[i][k] = an[i][k] = 0.f;
     if (kRing) {
         if (t == 0) {
             failed[0] = failed[1] = 0;
@@ -555,46 +557,34 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
                 }
             }
             if (p.dres) Raw<TR, kVec>::st(p.dres, row * p.dim + c, d[i]);
-            float n[kVec], z[kVec], w[kVec];
+            float n[kVec], z[kVec], w[kVec], sc[kVec];
             xr[i].get(n);
             if (p.gate != kGateNone) zr[i].get(z);
             if (before) {
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) n[k] *= silu_f32(z[k]);
             }
-            if (p.weight) {
-                ld_weight<kVec>(p.weight, c, w);
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) n[k] *= rstd;
-            }
-            if (p.res_scale) {
-                ld_weight<kVec>(p.res_scale, c, f);
+            for (int k = 0; k < kVec; ++k) w[k] = sc[k] = 1.f;
+            if (p.weight) ld_weight<kVec>(p.weight, c, w);
+            if (p.res_scale) ld_weight<kVec>(p.res_scale, c, sc);
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    float u = p.weight ? n[k] * w[k] : n[k];
-                    if (after) u *= silu_f32(z[k]);
-                    as[i][k] = fmaf(d[i][k], u, as[i][k]);
-                    d[i][k] *= f[k];
-                }
-            }
+            for (int k = 0; k < kVec; ++k) n[k] *= rstd;
             if (after) {
                 float dz[kVec];
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) {
                     const float sig = sigmoid_f32(z[k]);
-                    const float pp = p.weight ? n[k] * w[k] : n[k];
-                    dz[k] = d[i][k] * pp * sig * (1.f + z[k] * (1.f - sig));
+                    dz[k] = d[i][k] * sc[k] * (n[k] * w[k]) * sig * (1.f + z[k] * (1.f - sig));
                     d[i][k] *= z[k] * sig;
                 }
                 Raw<T, kVec>::st(p.dz, row * p.dim + c, dz);
             }
-            if (p.weight) {
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    aw[i][k] = fmaf(d[i][k], n[k], aw[i][k]);
-                    d[i][k] *= w[k];
-                    s_dn[0] = fmaf(d[i][k], n[k], s_dn[0]);
-                }
+            for (int k = 0; k < kVec; ++k) {
+                ab[i][k] = fmaf(d[i][k], n[k], ab[i][k]);
+                d[i][k] *= sc[k] * w[k];
+                s_dn[0] = fmaf(d[i][k], n[k], s_dn[0]);
             }
         }
         if (kRing) {
@@ -652,7 +642,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
         }
     }
     // the block's column sums; its row slots add theirs in turn
-    float *part = p.partial + (long long)blockIdx.x * 3 * p.dim;
+    float *part = p.partial + (long long)blockIdx.x * 2 * p.dim;
     if (m.rows_per > 1) {
         for (int s = 0; s < m.rows_per; ++s) {
             if (sub == s && grp < p.groups) {
@@ -663,15 +653,14 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
 #pragma unroll
                     for (int k = 0; k < kVec; ++k) {
                         const int c = grp * gs + e + k;
-                        sums[c] = (s ? sums[c] : 0.f) + aw[i][k];
-                        sums[p.dim + c] = (s ? sums[p.dim + c] : 0.f) + as[i][k];
-                        sums[2 * p.dim + c] = (s ? sums[2 * p.dim + c] : 0.f) + an[i][k];
+                        sums[c] = (s ? sums[c] : 0.f) + ab[i][k];
+                        sums[p.dim + c] = (s ? sums[p.dim + c] : 0.f) + an[i][k];
                     }
                 }
             }
             __syncthreads();
         }
-        for (int c = t; c < 3 * p.dim; c += blockDim.x) part[c] = sums[c];
+        for (int c = t; c < 2 * p.dim; c += blockDim.x) part[c] = sums[c];
         return;
     }
     if (grp < p.groups) {
@@ -680,33 +669,37 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormParams p, const Map m) {
             const int e = (i * m.tg + lane) * kVec;
             if (e >= gs) continue;
             const int c = grp * gs + e;
-            if (p.weight) Raw<float, kVec>::st(part, c, aw[i]);
-            if (p.res_scale) Raw<float, kVec>::st(part + p.dim, c, as[i]);
-            if (p.next_weight) Raw<float, kVec>::st(part + 2 * p.dim, c, an[i]);
+            if (p.weight || p.res_scale) Raw<float, kVec>::st(part, c, ab[i]);
+            if (p.next_weight) Raw<float, kVec>::st(part + p.dim, c, an[i]);
         }
     }
 }
 
 // Column sums over the n blocks' partials: 32 columns a block, 32 slices.
 __global__ void __launch_bounds__(1024)
-block_norm_reduce_kernel(const float *__restrict__ partial, int n, int dim, float *dweight,
-                         float *dres_scale, float *dnext_weight) {
+block_norm_reduce_kernel(const BlockNormParams p, int n) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
-    float *out = which == 0 ? dweight : which == 1 ? dres_scale : dnext_weight;
-    if (!out) return;
+    if (which ? !p.dnext_weight : !p.dweight && !p.dres_scale) return;
     float v = 0.f;
-    if (c < dim) {
+    if (c < p.dim) {
 #pragma unroll 8
-        for (int k = w; k < n; k += 32) v += partial[((long long)k * 3 + which) * dim + c];
+        for (int k = w; k < n; k += 32) v += p.partial[((long long)k * 2 + which) * p.dim + c];
     }
     s[w][lane] = v;
     __syncthreads();
     float u = s[lane][w];  // column w of the 32, slice `lane`
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
-    if (lane == 0 && blockIdx.x * 32 + w < dim) out[blockIdx.x * 32 + w] = u;
+    const int o = blockIdx.x * 32 + w;
+    if (lane != 0 || o >= p.dim) return;
+    if (which) {
+        p.dnext_weight[o] = u;
+    } else {
+        if (p.dweight) p.dweight[o] = p.res_scale ? u * p.res_scale[o] : u;
+        if (p.dres_scale) p.dres_scale[o] = p.weight ? u * p.weight[o] : u;
+    }
 }
 
 int pow2_floor(int v) {
@@ -827,15 +820,14 @@ cudaError_t bwd(const BlockNormParams &params, const Map &m, cudaStream_t stream
         }
     }
     if (!ring) {
-        const int smem = m.rows_per > 1 ? 3 * p.dim * (int)sizeof(float) : 0;
+        const int smem = m.rows_per > 1 ? 2 * p.dim * (int)sizeof(float) : 0;
         block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, false>
             <<<(unsigned)blocks, threads, smem, stream>>>(p, m);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(p.weight || p.res_scale || p.next_weight)) return e;
-    block_norm_reduce_kernel<<<dim3((unsigned)((p.dim + 31) / 32), 3), 1024, 0, stream>>>(
-        p.partial, (int)blocks, p.dim, p.weight ? p.dweight : nullptr,
-        p.res_scale ? p.dres_scale : nullptr, p.next_weight ? p.dnext_weight : nullptr);
+    block_norm_reduce_kernel<<<dim3((unsigned)((p.dim + 31) / 32), 2), 1024, 0, stream>>>(
+        p, (int)blocks);
     return cudaGetLastError();
 }
 

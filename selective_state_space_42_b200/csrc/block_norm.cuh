@@ -18,7 +18,7 @@ struct BlockNormParams {
     void *out, *y;                      // forward: [rows][dim], each may be NULL
     const void *dout, *dy;              // gradient: [rows][dim], each may be NULL
     void *dx, *dz, *dres;
-    float *partial;                     // [blocks][3][dim]: dweight, dres_scale, dnext_weight sums
+    float *partial;                     // [blocks][2][dim]: the sums behind dweight and dres_scale, dnext_weight's
     float *dweight, *dres_scale, *dnext_weight;
     long long rows;
     int dim, groups;

@@ -399,9 +399,9 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
         const float *src[2] = {reinterpret_cast<float *>(w + l.dq),
                                reinterpret_cast<float *>(w + l.dk)};
         void *dst[2] = {dq, dk_};
-        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
-            e = launch_linattn_group_sum(src[i], dst[i], d.tokens(), (int)qk_heads, group, (int)dk,
-                                         d.bf16, stream);
+        if (e == cudaSuccess)
+            e = launch_linattn_group_sums(src, dst, d.tokens(), (int)qk_heads, group, (int)dk,
+                                          d.bf16, stream);
     }
     if (want_dg && e == cudaSuccess) {
         LinattnDecayGrad g{};

@@ -469,8 +469,11 @@ linattn_carry_kernel(const __grid_constant__ LinattnParams p, unsigned blocks_pe
 
 template <typename T>
 __global__ void __launch_bounds__(kThr)
-linattn_group_sum_kernel(const float *__restrict__ src, T *__restrict__ dst, long long n, int group,
-                         int dim) {
+linattn_group_sum_kernel(const float *__restrict__ src0, T *__restrict__ dst0,
+                         const float *__restrict__ src1, T *__restrict__ dst1, long long n,
+                         int group, int dim) {
+    const float *src = blockIdx.y ? src1 : src0;
+    T *dst = blockIdx.y ? dst1 : dst0;
     for (long long e = (long long)blockIdx.x * kThr + threadIdx.x; e < n;
          e += (long long)gridDim.x * kThr) {
         const float *s = src + (e / dim) * group * dim + e % dim;
@@ -491,7 +494,6 @@ constexpr int kDgThr = 1024, kDgPer = 4;
 template <typename T>
 __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const LinattnDecayGrad p) {
     __shared__ double wsum[32];
-    __shared__ double carry_s;
     const long long bh = blockIdx.x, b = bh / p.heads;
     const int h = (int)(bh % p.heads), t = threadIdx.x, lane = t & 31, w = t >> 5;
     const long long len = p.seqlens
@@ -505,13 +507,9 @@ __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const Linatt
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     if (lane == 0) wsum[w] = x;
     __syncthreads();
-    if (t == 0) {
-        double s = 0.0;
-        for (int k = 0; k < 32; ++k) s += wsum[k];
-        carry_s = s;
-    }
-    __syncthreads();
-    double carry = carry_s;
+    double carry = wsum[lane];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) carry += __shfl_xor_sync(0xffffffffu, carry, m);
     const T *g = static_cast<const T *>(p.g) + b * p.seqlen * p.heads + h;
     T *out = static_cast<T *>(p.dg) + b * p.seqlen * p.heads + h;
     for (long long i = len + t; i < p.seqlen; i += kDgThr) out[i * p.heads] = from_f32<T>(0.f);
@@ -520,15 +518,20 @@ __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const Linatt
     for (long long end = len; end > 0; end -= kDgThr * kDgPer) {
         // thread t takes tokens end − 1 − 4·t − e
         double v[kDgPer];
+        float r[kDgPer], c[kDgPer], gt[kDgPer];  // every load before the first sum
+#pragma unroll
+        for (int e = 0; e < kDgPer; ++e) {
+            const long long i = end - 1 - (long long)kDgPer * t - e;
+            r[e] = i >= 0 ? rows[i] : 0.f;
+            c[e] = i >= 0 ? cols[i] : 0.f;
+            gt[e] = i >= 0 ? ldg_f32(g + i * p.heads) : 0.f;
+        }
         double s = 0.0;
 #pragma unroll
         for (int e = 0; e < kDgPer; ++e) {
             const long long i = end - 1 - (long long)kDgPer * t - e;
-            double d = 0.0;
-            if (i >= 0)
-                for (int k = 0; k < p.tiles; ++k)
-                    d += (double)rows[k * plane + i] - (double)cols[k * plane + i];
-            s += d;
+            s += (double)r[e] - (double)c[e];
+            if (p.tiles > 1 && i >= 0) s += (double)rows[plane + i] - (double)cols[plane + i];
             v[e] = s;
         }
         double incl = s;
@@ -540,18 +543,22 @@ __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const Linatt
         __syncthreads();  // wsum's readers of the previous tile are done
         if (lane == 31) wsum[w] = incl;
         __syncthreads();
-        double before = 0.0, total = 0.0;
-        for (int k = 0; k < 32; ++k) {
-            if (k == w) before = total;
-            total += wsum[k];
+        double sums = wsum[lane];  // of the warps up to warp `lane`
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, sums, m);
+            if (lane >= m) sums += o;
         }
+        const double total = __shfl_sync(0xffffffffu, sums, 31);
+        double before = __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
+        if (w == 0) before = 0.0;
         const double base = carry + before + (incl - s);
 #pragma unroll
         for (int e = 0; e < kDgPer; ++e) {
             const long long i = end - 1 - (long long)kDgPer * t - e;
             if (i < 0) continue;
             const bool none = (i == 0 && !p.has_init) ||
-                              (double)ldg_f32(g + i * p.heads) * 1.4426950408889634 < kLaResetLog2;
+                              (double)gt[e] * 1.4426950408889634 < kLaResetLog2;
             out[i * p.heads] = from_f32<T>(none ? 0.f : (float)(base + v[e]));
         }
         carry += total;
@@ -630,16 +637,19 @@ cudaError_t launch_linattn_carry(const LinattnParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_linattn_group_sum(const float *src, void *dst, long long tokens, int qk_heads,
-                                     int group, int dim, bool bf16, cudaStream_t stream) {
+cudaError_t launch_linattn_group_sums(const float *const src[2], void *const dst[2],
+                                      long long tokens, int qk_heads, int group, int dim, bool bf16,
+                                      cudaStream_t stream) {
     const long long n = tokens * qk_heads * dim;
-    const unsigned blocks = (unsigned)std::min((n + kThr - 1) / kThr, 1ll << 20);
+    const dim3 grid((unsigned)std::min((n + kThr - 1) / kThr, 1ll << 20), 2);
     if (bf16)
-        linattn_group_sum_kernel<<<blocks, kThr, 0, stream>>>(
-            src, static_cast<__nv_bfloat16 *>(dst), n, group, dim);
+        linattn_group_sum_kernel<<<grid, kThr, 0, stream>>>(
+            src[0], static_cast<__nv_bfloat16 *>(dst[0]), src[1],
+            static_cast<__nv_bfloat16 *>(dst[1]), n, group, dim);
     else
-        linattn_group_sum_kernel<<<blocks, kThr, 0, stream>>>(src, static_cast<float *>(dst), n,
-                                                              group, dim);
+        linattn_group_sum_kernel<<<grid, kThr, 0, stream>>>(src[0], static_cast<float *>(dst[0]),
+                                                            src[1], static_cast<float *>(dst[1]),
+                                                            n, group, dim);
     return cudaGetLastError();
 }
 

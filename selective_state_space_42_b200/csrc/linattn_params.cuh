@@ -135,10 +135,11 @@ cudaError_t linattn_launch(Kernel full, Kernel state, int threads, int smem_full
 bool linattn_tc_rows(const void *ptr, long long row, int dim, long long seqlen);
 cudaError_t launch_linattn_tc(const LinattnParams &p, cudaStream_t stream);
 
-// Sum of the `group` heads that share one query/key head:
+// Sums of the `group` heads that share one query/key head, of dq and of dk:
 // src [tokens][qk_heads][group][dim] float32 -> dst [tokens][qk_heads][dim].
-cudaError_t launch_linattn_group_sum(const float *src, void *dst, long long tokens, int qk_heads,
-                                     int group, int dim, bool bf16, cudaStream_t stream);
+cudaError_t launch_linattn_group_sums(const float *const src[2], void *const dst[2],
+                                      long long tokens, int qk_heads, int group, int dim, bool bf16,
+                                      cudaStream_t stream);
 
 // dlog_decay from the per-token dot products (rows = q·dq, cols = k·dk, each
 // `tiles` partial sums of [batch][heads][seqlen]) and, when dfinal is given,

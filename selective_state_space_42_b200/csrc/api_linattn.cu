@@ -391,6 +391,7 @@ int selscan_linattn_bwd(const void *q, const void *k, const void *v, float scale
         a.y = dv_;
         a.h_init = dfinal_state;
         a.h_final = dinitial_state;
+        a.fine_state = dinitial_state != nullptr;
     }
     cudaError_t e = device_status_address(&p.status);
     if (e == cudaSuccess)

@@ -35,6 +35,7 @@ struct SweepArgs {
     const float *h_init;          // [batch][heads][dk][dv] (h_init_t: [dv][dk]) or NULL: the state entering
     float *h_final;               // likewise, the state leaving, or NULL
     int h_init_t, h_final_t;
+    int fine_state;               // h_final is a result of the call: its sums keep 24 bits
     float *seg_state;             // [batch·heads][nseg][dk][dv]: segments' states
     float *seg_decay;             // [batch·heads][nseg]
     int map[4], map_y;            // tensor-core path: tensor maps of q, k, v, dot and y

@@ -30,7 +30,9 @@
 // carried over the whole sequence, keeps 24 bits. The gradient needs its
 // products with S_in to about 16 bits instead (its log decays' gradient sums
 // q·dq − k·dk, which cancel), so there S_in is a high/low pair and c ◦ V two
-// parts (17 bits): both fill the 512 columns of tensor memory.
+// parts (17 bits): both fill the 512 columns of tensor memory. The last state of the
+// sweep for dv is a float32 result where the first state's gradient is asked for:
+// there c ◦ V has three parts too, the third in the scores' columns.
 //
 // Bound: a chunk's chain of scores, P, output product and store, and of c ◦ V, U and
 // state: 2.7 µs a chunk at D = 128 (3.4 in the gradient, 1.6 in the pass over states)
@@ -216,17 +218,23 @@ __device__ __forceinline__ uint32_t tile_off(int j, int d) {
 // chunk uses, and the third in the last columns.
 template <int D, bool kBwd, bool kFull> struct Cols {
     static constexpr uint32_t S = 0, Yi = 64, Ye = 128, U = kFull ? 192 : 0;
-    static constexpr uint32_t St = 192 + D, StParts = kBwd ? 2 : 1;
-    static constexpr uint32_t VpParts = kBwd ? 2 : 3;
-    static constexpr uint32_t Vp = kFull ? St + StParts * (D / 2) : 2 * D;
+    static constexpr uint32_t St = 192 + D;
+    // A gradient's sweep has two parts of c ◦ V or, where its last state is a result
+    // (`fine`), three: at D = 128 the third lies where S does, once S has been read.
+    static constexpr uint32_t StParts = kBwd ? 2 : 1;
+    static constexpr bool VpOnS = kFull && kBwd && D == 128;
+    static __device__ __forceinline__ int vp_parts(bool fine) { return kBwd && !fine ? 2 : 3; }
     static constexpr int UBufs = kFull ? 1 : 2, VpBufs = kFull && kBwd ? 1 : 2;
     static constexpr bool VpOnYe = kFull && !kBwd && D == 128;
-    static constexpr uint32_t VpNext = VpParts * 32;
+    static constexpr uint32_t VpNext = 96;
+    static constexpr uint32_t Vp = kFull ? St + StParts * (D / 2) : 2 * D;
     static __device__ __forceinline__ uint32_t vp(int buf, int part) {
         if (VpOnYe && buf) return part < 2 ? Ye + 32 * part : Vp + VpNext;
+        if (VpOnS && part == 2) return S;
         return Vp + buf * VpNext + part * 32;
     }
-    static_assert(Vp + (VpOnYe ? VpNext + 32 : VpBufs * VpNext) <= 512, "tensor memory");
+    static_assert(Vp + (VpOnYe ? VpNext + 32 : VpOnS ? 64 : VpBufs * VpNext) <= 512,
+                  "tensor memory");
 };
 
 template <int D, bool kBwd, bool kFull> struct TcSmem {
@@ -372,8 +380,10 @@ __device__ __forceinline__ void output_rows(uint32_t t_y, uint32_t t_ye, bf16 *o
 }
 
 // One block: one (sweep, batch row, head, segment). kFull false: only the
-// segment's own state, from zero.
-template <int D, bool kBwd, bool kFull>
+// segment's own state, from zero. kFine: some sweeps have three parts of c ◦ V (one
+// kernel for both cost the gradient without them 224 → 257 µs on 2 × 4096 tokens of
+// 16 heads of 128, in registers and code).
+template <int D, bool kBwd, bool kFull, bool kFine>
 __global__ void __launch_bounds__(kThr, 1)
 linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant__ TcMaps maps) {
     typedef TcSmem<D, kBwd, kFull> Smem;
@@ -399,6 +409,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     auto chunk_of = [&](int i) { return rev ? c_live - 1 - i : c_first + i; };
     const int t = threadIdx.x, lane = t & 31, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
     const bool has_dot = kBwd && kFull && a.dot_out != nullptr;
+    const bool fine = kFine && a.fine_state != 0;
+    const int nvp = C::vp_parts(fine);
 
     if (warp == kWarpTma) tmem_alloc(&S.tmem, 512);
     if (t == 0) {
@@ -586,18 +598,24 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (elect_one()) {
                     const uint32_t u = tmem + C::U + ub * D;
 #pragma unroll
-                    for (int part = 0; part < (int)C::VpParts; ++part)
+                    for (int part = 0; part < 3; ++part) {
+                        if (part >= nvp) break;
 #pragma unroll
                         for (int x = 0; x < kC / 16; ++x)
-                            umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok, id_u,
-                                         part > 0 || x > 0);
+                            umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok,
+                                         id_u, part > 0 || x > 0);
+                    }
                     umma_commit(&S.u_full[ub]);
                     if (kVBufs != kUBufs) umma_commit(&S.vp_empty[vb]);
                     if (!kFull) umma_commit(&S.empty[s]);
                 }
                 __syncwarp();
                 if (!kFull) continue;
-                if (i + 1 < n) scores(i + 1);
+                if (i + 1 < n) {
+                    // U reads c ◦ V's third part from where the scores go
+                    if (C::VpOnS && fine && !wait2(&S.u_full[ub], i, &S.u_full[ub], i)) break;
+                    scores(i + 1);
+                }
                 // Ye = S_inᵀ Qᵀ and Yi = Vᵀ Pᵀ, the second on top of the first where the row
                 // factors stand in the outputs
                 const bool two = kBwd || S.strong[i % kSlots] != 0;
@@ -736,10 +754,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                                 w + 32 * th + 16 * cp + 8 * (k >> 1) + c2);
                             float x0 = f.x * bf_lo(v[k]), x1 = f.y * bf_hi(v[k]);
 #pragma unroll
-                            for (int e = 0; e < (int)C::VpParts; ++e) {
+                            for (int e = 0; e < 3; ++e) {
+                                if (e >= nvp) break;
                                 // all parts but the last by truncation (no conversion)
                                 const uint32_t u =
-                                    e + 1 < (int)C::VpParts
+                                    e + 1 < nvp
                                         ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
                                         : pack_bf16x2(x0, x1);
                                 part[e][4 * cp + k] = u;
@@ -752,6 +771,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (q == 0 && use > 0) {
                     // U has read what stands there
                     ok = wait(kVBufs == kUBufs ? &S.u_full[vb] : &S.vp_empty[vb], use - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (C::VpOnS && fine && q == 0) {
+                    ok = wait(&S.s_empty, i);  // the chunk's scores have been read
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -770,10 +794,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 }
                 if (d0 < D) {
 #pragma unroll
-                    for (int e = 0; e < (int)C::VpParts; ++e)
-                        tmem_st_frag(tmem + lanes + ((uint32_t)(16 * hh) << 16) + C::vp(vb, e) +
-                                         16 * th,
-                                     part[e]);
+                    for (int e = 0; e < 3; ++e)
+                        if (e < nvp)
+                            tmem_st_frag(tmem + lanes + ((uint32_t)(16 * hh) << 16) +
+                                             C::vp(vb, e) + 16 * th,
+                                         part[e]);
                 }
             }
             if (!ok) break;
@@ -985,12 +1010,12 @@ bool make_map(CUtensorMap *m, const void *base, long long batch, long long seqle
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kBwd>
+template <int D, bool kBwd, bool kFine>
 cudaError_t launch(const LinattnParams &p, const TcMaps &maps, cudaStream_t stream) {
     const int smem = (int)sizeof(TcSmem<D, kBwd, true>) + 1024;
     const int smem_own = (int)sizeof(TcSmem<D, kBwd, false>) + 1024;
-    auto full = linattn_tc_kernel<D, kBwd, true>;
-    auto state = linattn_tc_kernel<D, kBwd, false>;
+    auto full = linattn_tc_kernel<D, kBwd, true, kFine>;
+    auto state = linattn_tc_kernel<D, kBwd, false, kFine>;
     cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_own);
@@ -1047,8 +1072,15 @@ cudaError_t launch_linattn_tc(const LinattnParams &params, cudaStream_t stream) 
         a.map_y = n++;
     }
     if (p.nsweeps == 1)
-        return most <= 64 ? launch<64, false>(p, maps, stream) : launch<128, false>(p, maps, stream);
-    return most <= 64 ? launch<64, true>(p, maps, stream) : launch<128, true>(p, maps, stream);
+        return most <= 64 ? launch<64, false, false>(p, maps, stream)
+                          : launch<128, false, false>(p, maps, stream);
+    bool fine = false;
+    for (int i = 0; i < p.nsweeps; ++i) fine = fine || p.sweep[i].fine_state;
+    if (fine)
+        return most <= 64 ? launch<64, true, true>(p, maps, stream)
+                          : launch<128, true, true>(p, maps, stream);
+    return most <= 64 ? launch<64, true, false>(p, maps, stream)
+                      : launch<128, true, false>(p, maps, stream);
 }
 
 }  // namespace selscan

@@ -421,6 +421,24 @@ def test_growing_states_and_one_state_given(dtype, given):
     check_bwd(i, dtype, what="growing")
 
 
+@pytest.mark.parametrize("d", [48, 64, 128])
+def test_states_of_bfloat16_operands_keep_float32(d):
+    """The float32 results of bfloat16 operands, the last state and the first
+    one's gradient, to 2^-18 of their size: over five chunks the decays and a
+    token's weight are ten exponentials of 2^-22 at most, and the sums of 320 terms
+    round by less than six more together."""
+    i = make(2, 300, 2, 2, d, d, "bf16", 32, h0=True, strength=0.02)
+    v = dev(i)
+    n = gh.to_np
+    a = (n(i["q"]), n(i["k"]), n(i["v"]), n(i["g"]), d ** -0.5, n(i["h0"]), None)
+    _, S = ss.selscan_linattn_fwd(v["q"], v["k"], v["v"], v["g"], initial_state=v["h0"],
+                                  return_final_state=True)
+    gh.compare(n(S), lo.linattn_fwd(*a)[1], 2.0 ** -18, "state")
+    g = ss.selscan_linattn_bwd(v["q"], v["k"], v["v"], v["g"], initial_state=v["h0"],
+                               dy=v["dy"], dfinal_state=v["dS"])
+    gh.compare(n(g["dh0"]), lo.linattn_bwd(*a, n(i["dy"]), n(i["dS"]))["dh0"], 2.0 ** -18, "dh0")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_one_tensor_for_all_operands(dtype):
     d = dev(make(1, 150, 2, 2, 64, 64, dtype, 31))

@@ -153,7 +153,7 @@ def test_block_norm_bwd_validation(lib):
     assert call(ws=P + (1 << 24), wsb=16) == -8
     assert lib.selscan_block_norm_bwd_workspace_bytes(0, 16) == 0
     assert lib.selscan_block_norm_bwd_workspace_bytes(5, 16385) == 0
-    assert lib.selscan_block_norm_bwd_workspace_bytes(5, 64) == 5 * 3 * 64 * 4  # a block a row
+    assert lib.selscan_block_norm_bwd_workspace_bytes(5, 64) == 5 * 2 * 64 * 4  # a block a row
 
 
 def test_bindings_refuse_cpu_tensors_and_wrong_shapes(lib):

@@ -22,6 +22,7 @@
 #include "tma_util.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 #include "api_util.cuh"
 
@@ -761,20 +762,35 @@ int plan_ring(BlockNormParams *p, size_t es, size_t rs, bool bwd, long long bloc
     return p->stages;
 }
 
+// A ring may take kRoom bytes whatever this call's stages come to: the opt-in belongs to
+// the function and the device, so a call's own size set here would shrink it under a
+// launch that another host thread is about to make with more. Set once per device.
+template <int kRoom, typename Kernel>
+cudaError_t allow_ring(Kernel kernel, std::atomic<unsigned long long> &configured) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (configured.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
 cudaError_t fwd(const BlockNormParams &params, const Map &m, cudaStream_t stream) {
     BlockNormParams p = params;
     const int threads = m.row_threads * m.rows_per;
     if constexpr (kVec == 8) {
         // two blocks an SM, 100 KB of rows on their way to each
+        constexpr int kRoom = 100 << 10;
         const long long blocks = 2ll * sm_count();
-        if (m.rows_per == 1 && plan_ring(&p, sizeof(T), sizeof(TR), false, blocks, 100 << 10)) {
+        if (m.rows_per == 1 && plan_ring(&p, sizeof(T), sizeof(TR), false, blocks, kRoom)) {
             auto k = block_norm_fwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, true>;
-            const int smem = p.stages * p.stage_bytes;
-            const cudaError_t e =
-                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            static std::atomic<unsigned long long> configured{0};
+            const cudaError_t e = allow_ring<kRoom>(k, configured);
             if (e != cudaSuccess) return e;
-            k<<<(unsigned)blocks, threads, smem, stream>>>(p, m);
+            k<<<(unsigned)blocks, threads, p.stages * p.stage_bytes, stream>>>(p, m);
             return cudaGetLastError();
         }
     }
@@ -806,17 +822,17 @@ cudaError_t bwd(const BlockNormParams &params, const Map &m, cudaStream_t stream
         std::min<long long>(want, block_norm_bwd_blocks(p.rows, std::max(threads, 128)));
     bool ring = false;
     if constexpr (kVec == 8) {
+        constexpr int kRoom = kBlocks == 2 ? 100 << 10 : 200 << 10;
         const long long two = (long long)kBlocks * sm_count();
         if (m.rows_per == 1 && two <= blocks &&
-            plan_ring(&p, sizeof(T), sizeof(TR), true, two, kBlocks == 2 ? 100 << 10 : 200 << 10)) {
+            plan_ring(&p, sizeof(T), sizeof(TR), true, two, kRoom)) {
             ring = true;
             blocks = two;
             auto k = block_norm_bwd_kernel<T, TR, kVec, kNV, kThreads, kBlocks, true>;
-            const int smem = p.stages * p.stage_bytes;
-            const cudaError_t e =
-                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            static std::atomic<unsigned long long> configured{0};
+            const cudaError_t e = allow_ring<kRoom>(k, configured);
             if (e != cudaSuccess) return e;
-            k<<<(unsigned)blocks, threads, smem, stream>>>(p, m);
+            k<<<(unsigned)blocks, threads, p.stages * p.stage_bytes, stream>>>(p, m);
         }
     }
     if (!ring) {

@@ -488,12 +488,19 @@ linattn_group_sum_kernel(const float *__restrict__ src0, T *__restrict__ dst0,
 // dg_t + k_t·dk_t and q_t·dq_t + dg_{t+1}. The running sum is kept in double:
 // its terms cancel over the sequence, so dg carries the float32 errors of the
 // dot products it sums. Where exp(g_t)·S_{t−1} is zero (a reset; the first
-// token without a first state) dg is zero. One block per (batch row, head), tokens
-// from the last to the first in tiles of 4·1024.
+// token without a first state) dg is zero, and the sum starts from nothing
+// again at a reset: neither the errors nor a NaN of what stands behind it
+// reach the tokens before. A reset here is a factor that the sweeps' ex2.approx
+// flushes to zero, below 2^−126. One block per (batch row, head), tokens from
+// the last to the first in tiles of 4·1024; a partial sum goes with a flag that
+// says whether it begins at a reset, and one with the flag takes nothing from
+// before.
 constexpr int kDgThr = 1024, kDgPer = 4;
+constexpr double kDgResetLog2 = -126.0;
 template <typename T>
 __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const LinattnDecayGrad p) {
     __shared__ double wsum[32];
+    __shared__ int wreset[32];
     const long long bh = blockIdx.x, b = bh / p.heads;
     const int h = (int)(bh % p.heads), t = threadIdx.x, lane = t & 31, w = t >> 5;
     const long long len = p.seqlens
@@ -527,41 +534,65 @@ __global__ void __launch_bounds__(kDgThr) linattn_decay_grad_kernel(const Linatt
             gt[e] = i >= 0 ? ldg_f32(g + i * p.heads) : 0.f;
         }
         double s = 0.0;
+        bool reset = false;  // s begins at a reset among the thread's tokens
+        bool own[kDgPer];    // and so does v[e]
 #pragma unroll
         for (int e = 0; e < kDgPer; ++e) {
             const long long i = end - 1 - (long long)kDgPer * t - e;
             s += (double)r[e] - (double)c[e];
             if (p.tiles > 1 && i >= 0) s += (double)rows[plane + i] - (double)cols[plane + i];
+            if ((double)gt[e] * 1.4426950408889634 < kDgResetLog2) {
+                s = 0.0;
+                reset = true;
+            }
             v[e] = s;
+            own[e] = reset;
         }
         double incl = s;
+        int from = reset;
+        auto scan = [&](double &sum, int &flag) {  // over the warp, later tokens first
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, incl, m);
-            if (lane >= m) incl += o;
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(0xffffffffu, sum, m);
+                const int f = __shfl_up_sync(0xffffffffu, flag, m);
+                if (lane >= m) {
+                    if (!flag) sum += o;
+                    flag |= f;
+                }
+            }
+        };
+        scan(incl, from);
+        __syncthreads();  // the readers of the previous tile's sums are done
+        if (lane == 31) {
+            wsum[w] = incl;
+            wreset[w] = from;
         }
-        __syncthreads();  // wsum's readers of the previous tile are done
-        if (lane == 31) wsum[w] = incl;
         __syncthreads();
         double sums = wsum[lane];  // of the warps up to warp `lane`
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, sums, m);
-            if (lane >= m) sums += o;
+        int froms = wreset[lane];
+        scan(sums, froms);
+        // what stands before this thread's tokens: its warp's lanes, the warps, the tiles
+        double base = __shfl_up_sync(0xffffffffu, incl, 1);
+        int base_from = __shfl_up_sync(0xffffffffu, from, 1);
+        if (lane == 0) {
+            base = 0.0;
+            base_from = 0;
         }
-        const double total = __shfl_sync(0xffffffffu, sums, 31);
-        double before = __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
-        if (w == 0) before = 0.0;
-        const double base = carry + before + (incl - s);
+        const double before = __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
+        const int before_from = __shfl_sync(0xffffffffu, froms, (w + 31) & 31);
+        if (!base_from) {
+            if (w > 0) base += before;
+            if (w == 0 || !before_from) base += carry;
+        }
 #pragma unroll
         for (int e = 0; e < kDgPer; ++e) {
             const long long i = end - 1 - (long long)kDgPer * t - e;
             if (i < 0) continue;
-            const bool none = (i == 0 && !p.has_init) ||
-                              (double)gt[e] * 1.4426950408889634 < kLaResetLog2;
-            out[i * p.heads] = from_f32<T>(none ? 0.f : (float)(base + v[e]));
+            const bool none = i == 0 && !p.has_init;
+            out[i * p.heads] = from_f32<T>(none ? 0.f : (float)(own[e] ? v[e] : base + v[e]));
         }
-        carry += total;
+        const double total = __shfl_sync(0xffffffffu, sums, 31);
+        carry = __shfl_sync(0xffffffffu, froms, 31) ? total : carry + total;
     }
 }
 

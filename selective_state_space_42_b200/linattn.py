@@ -165,7 +165,9 @@ def selscan_linattn_bwd(q, k, v, log_decay=None, scale=None, initial_state=None,
             dq=torch.empty(B, L, Hq, dk, device=dev, dtype=dt),
             dk=torch.empty(B, L, Hq, dk, device=dev, dtype=dt),
             dv=torch.empty(B, L, H, dv, device=dev, dtype=dt),
-            dlog_decay=torch.empty(B, L, H, device=dev, dtype=dt) if opts.log_decay else None,
+            # by the argument: an empty tensor's pointer is NULL
+            dlog_decay=torch.empty(B, L, H, device=dev, dtype=dt)
+            if log_decay is not None and log_decay.dim() == 3 else None,
             dh0=None if initial_state is None
             else torch.empty(B, H, dk, dv, device=dev, dtype=torch.float32))
         nbytes = _workspace("selscan_linattn_bwd_workspace_bytes", dev.index, *sizes, code)

@@ -246,7 +246,9 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     bf16 P[kFull ? kC * kC : 8];
     bf16 out[kFull ? kC * D : 8];   // y on its way out: swizzled slabs of 64 columns
     float A[kSlots][kC];            // log2 of the row factors without their scale
-    float rowf[kSlots][kC], colf[kSlots][kC], colw[kSlots][kC];
+    float rowf[kSlots][kC];
+    float colf[kSlots][kC];         // column factors of P; in a strong chunk those of A's rounding
+    float colw[kSlots][kC];
     float decay[kSlots];
     int strong[kSlots];             // the factors of P leave float32's comfortable range
     float red[4][kC];
@@ -260,24 +262,50 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     int abort;
 };
 
+// Two floats at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // 32 columns of a row of P as packed bfloat16: scores times f_j (kRow: times
-// `row` too); in a strong chunk times row·2^(a − f_j), f the columns' A. Zero
-// outside columns lo .. hi. Selects, not branches.
+// `row` too); in a strong chunk times row·f_j·2^(a − A_j). Zero outside columns
+// lo .. hi. Selects, not branches.
 template <bool kRow, bool kStrong>
-__device__ __forceinline__ void score_weights(const float (&v)[32], const float *f, float row,
-                                              float a, int lo, int hi, uint32_t (&out)[16]) {
+__device__ __forceinline__ void score_weights(const float (&v)[32], const float *f, const float *A,
+                                              float row, float a, int lo, int hi,
+                                              uint32_t (&out)[16]) {
 #pragma unroll
     for (int e4 = 0; e4 < 8; ++e4) {
         const float4 f4 = *reinterpret_cast<const float4 *>(f + 4 * e4);
-        const float g[4] = {f4.x, f4.y, f4.z, f4.w};
         float x[4];
+        if (kStrong) {
+            const float4 h4 = *reinterpret_cast<const float4 *>(A + 4 * e4);
+            const float h[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = 4 * e4 + e;
-            float w = kStrong ? ex2_approx(a - g[e]) : g[e];
-            if (kRow || kStrong) w *= row;
-            w *= v[j];
-            x[e] = j >= lo && j <= hi ? w : 0.f;
+            for (int e = 0; e < 4; e += 2) {
+                const int j = 4 * e4 + e;
+                float2 w = make_float2(ex2_approx(a - h[e]), ex2_approx(a - h[e + 1]));
+                w = mul2(mul2(w, e ? make_float2(f4.z, f4.w) : make_float2(f4.x, f4.y)),
+                         mul2(make_float2(row, row), make_float2(v[j], v[j + 1])));
+                x[e] = j >= lo && j <= hi ? w.x : 0.f;
+                x[e + 1] = j + 1 >= lo && j + 1 <= hi ? w.y : 0.f;
+            }
+        } else {
+            const float g[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 4 * e4 + e;
+                float w = g[e];
+                if (kRow) w *= row;
+                w *= v[j];
+                x[e] = j >= lo && j <= hi ? w : 0.f;
+            }
         }
         out[2 * e4] = pack_bf16x2(x[0], x[1]);
         out[2 * e4 + 1] = pack_bf16x2(x[2], x[3]);
@@ -517,17 +545,26 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 // A: the log2 of what separates a token from the state entering (in the sweep's
                 // direction); a pair's weight is 2^(A_row − A_col)
                 const double G[2] = {sum - g1, sum};
+                double exact[2];
                 float A[2], row[2], colf[2], colw[2];
                 bool far = false;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    A[e] = (float)(rev ? end - G[e] : G[e]);
+                    exact[e] = rev ? end - G[e] : G[e];
+                    A[e] = (float)exact[e];
                     far = far || !(fabsf(A[e]) <= kRange);
                     row[e] = a.row_scale * ex2_approx(A[e]);
                     colf[e] = a.col_scale * ex2_approx(-A[e]);
                     colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
                 }
                 far = __any_sync(0xffffffffu, far);
+                if (far) {
+                    // A strong chunk's weights are 2^(A_row − A_col) from A as it is rounded
+                    // (a step of 2^-10 behind many resets, where it passes 2^13; the
+                    // difference itself is exact there) and the factors of what it lost.
+                    colf[0] = ex2_approx((float)((double)A[0] - exact[0]));
+                    colf[1] = ex2_approx((float)((double)A[1] - exact[1]));
+                }
                 const int sl = i % kSlots;
                 *reinterpret_cast<float2 *>(&S.A[sl][2 * lane]) = make_float2(A[0], A[1]);
                 *reinterpret_cast<float2 *>(&S.rowf[sl][2 * lane]) = make_float2(row[0], row[1]);
@@ -661,7 +698,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     if (!ok) break;
                     tc_fence_after();
                     const bool strong = S.strong[sl] != 0;
-                    const float rf = S.rowf[sl][r], ar = S.A[sl][r], both = a.row_scale * a.col_scale;
+                    const float rf = S.rowf[sl][r], ar = S.A[sl][r];
+                    // in a strong chunk: the reciprocal of a factor within 2^-11.5 of one, to 2^-23
+                    const float low = a.p_scale * (2.f - S.colf[sl][r]);
                     const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
                     char *row = reinterpret_cast<char *>(S.P) + r * 128;
                     uint32_t out[16];
@@ -672,12 +711,13 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                             tc_fence_before();
                             arrive(&S.s_empty);  // the next chunk's scores may come
                         }
+                        const float *f = S.colf[sl] + 32 * half;
                         if (strong)
-                            score_weights<true, true>(v, S.A[sl] + 32 * half, both, ar, lo - 32 * half,
-                                                      hi - 32 * half, out);
+                            score_weights<true, true>(v, f, S.A[sl] + 32 * half, low, ar,
+                                                      lo - 32 * half, hi - 32 * half, out);
                         else
-                            score_weights<kBwd, false>(v, S.colf[sl] + 32 * half, rf, 0.f,
-                                                       lo - 32 * half, hi - 32 * half, out);
+                            score_weights<kBwd, false>(v, f, nullptr, rf, 0.f, lo - 32 * half,
+                                                       hi - 32 * half, out);
                     };
                     // the block off the diagonal (of the warp that has one, else zeros), then
                     // the one on it

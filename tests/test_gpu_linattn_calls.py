@@ -1,11 +1,13 @@
 """Calls of linear attention that its documentation allows and whose answers are
 easy to lose. Tolerances as in test_gpu_linattn.py unless stated."""
+import math
+
 import pytest
 import torch
 
 import selective_state_space_42_b200 as ss
 
-from test_gpu_linattn import DEV, DT
+from test_gpu_linattn import DEV, DT, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -17,3 +19,26 @@ def test_empty_decays_have_an_empty_gradient(dtype, shape):
     g = ss.selscan_linattn_bwd(z, z, z, z[..., 0].contiguous(), dy=z)
     assert g["dlog_decay"] is not None and g["dlog_decay"].shape == shape[:3]
     assert ss.selscan_linattn_bwd(z, z, z, torch.zeros(3, device=DEV), dy=z)["dlog_decay"] is None
+
+
+@pytest.mark.parametrize("op", ["y", "dq"])
+def test_weights_behind_many_resets(op):
+    """Tokens 45 .. 63 of a chunk whose first 45 all reset, against the same tokens
+    behind 44 that do nothing and one that resets. The pairs' weights are the same
+    up to 2^-20 (two exponentials of 2^-22 and a difference); at a step of 2^-8 of
+    the operand they are rounded to, that turns a rounding in 2^-11 of the pairs, at
+    most 19 pairs a row: 1% of the rows, of which twice as many are allowed."""
+    i = make(4, 64, 8, 8, 64, 64, "bf16", 61, strength=0.05)
+    d = dev(i)
+    many, one = d["g"].clone(), d["g"].clone()
+    many[:, :45] = -math.inf
+    one[:, :44] = 0
+    one[:, 44] = -math.inf
+
+    def run(g):
+        if op == "y":
+            return ss.selscan_linattn_fwd(d["q"], d["k"], d["v"], g)[:, 45:]
+        return ss.selscan_linattn_bwd(d["q"], d["k"], d["v"], g, dy=d["dy"])["dq"][:, 45:]
+
+    a, b = run(many), run(one)
+    assert (a != b).any(-1).float().mean().item() <= 0.02

@@ -14,7 +14,7 @@
 // accumulator. The gradient keeps the row factor in P and the products apart: its
 // sweeps for dq and dk must round the same weights the same way (their dot
 // products cancel in the log decays' gradient). So does, with an exponential per
-// score, a chunk whose factors leave 2^±60 (a reset, a few tokens of strong decay).
+// score, a chunk whose factors leave 2^±32 (a reset, a few tokens of strong decay).
 // Q, K, V (and in the gradient the operand of the dot product) come by TMA into
 // a ring of stages, 128-byte swizzled; P is written to shared memory; S_in and
 // c ◦ V are A operands in tensor memory. Warps (20, one block an SM):
@@ -53,7 +53,7 @@ constexpr int kC = kLaChunk;
 constexpr long long kWaitClocks = 4000000000ll;  // every wait gives up after about 2 s
 constexpr int kStatusLinattnWait = 6;         // device error code
 constexpr int kThr = 640;
-constexpr float kRange = 60.f;                // |log2| a chunk's split factors may reach
+constexpr float kRange = 32.f;                // |log2| a chunk's split factors may reach
 constexpr int kWarpTma = 2, kWarpMma = 3;
 constexpr int kMaps = 8;
 

@@ -7,7 +7,7 @@ import torch
 
 import selective_state_space_42_b200 as ss
 
-from test_gpu_linattn import DEV, DT, dev, make
+from test_gpu_linattn import DEV, DT, check_fwd, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,14 @@ def test_weights_behind_many_resets(op):
 
     a, b = run(many), run(one)
     assert (a != b).any(-1).float().mean().item() <= 0.02
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_products_under_decay(dtype):
+    """Scores of 2^62 times values of 2^26, and decays of 2^-51 over a chunk: every
+    result is within float32's range, so no factor on the way may leave it."""
+    i = make(1, 130, 2, 2, 64, 64, dtype, 60)
+    for k, e in (("q", 28), ("k", 28), ("v", 26)):
+        i[k] = (i[k].float() * 2.0 ** e).to(i[k].dtype)
+    i["g"][:] = -0.5546875
+    check_fwd(i, dtype, what="large")

@@ -84,15 +84,21 @@ __device__ __forceinline__ void st4(__nv_bfloat16 *p, const float4 &v) {
                                                *reinterpret_cast<const uint32_t *>(&hi));
 }
 
+__device__ __forceinline__ bool all_finite(const float4 &v) {
+    // products with zero: zero, or NaN
+    return fmaf(0.f, v.x, 0.f * v.y) + fmaf(0.f, v.z, 0.f * v.w) == 0.f;
+}
+
 // A [nq tokens][n columns] tile into shared memory as [column][token], zero
 // outside. Lanes run over tokens, so that the transposed stores hit distinct
 // banks; the four elements a lane reads per step share a sector with its
-// next step's.
+// next step's. True if the thread met a value that is not finite.
 template <typename T, int DKP>
-__device__ __forceinline__ void load_transposed(float (*dst)[kLd], const T *base, long long row,
+__device__ __forceinline__ bool load_transposed(float (*dst)[kLd], const T *base, long long row,
                                                 int nq, int n, bool vec) {
     const int tok = threadIdx.x & (kC - 1), grp = threadIdx.x / kC;
     const T *r = base + tok * row;
+    bool odd = false;
 #pragma unroll
     for (int it = 0; it < DKP / 16; ++it) {
         const int d = 4 * (grp + 4 * it);
@@ -101,7 +107,9 @@ __device__ __forceinline__ void load_transposed(float (*dst)[kLd], const T *base
         dst[d + 1][tok] = v.y;
         dst[d + 2][tok] = v.z;
         dst[d + 3][tok] = v.w;
+        odd = odd || !all_finite(v);
     }
+    return odd;
 }
 
 __device__ __forceinline__ void fma4(float4 &a, float s, const float4 &b) {
@@ -228,15 +236,17 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
         const int nl = (int)min((long long)kC, p.seqlen - t0);
         if (nq == 0 && !kFull) continue;
         __syncthreads();  // the tiles' readers of the previous chunk are done
+        bool odd = false;  // k or v holds a value that is not finite
         if (nq > 0) {
             if (kFull) load_transposed<T, DKP>(S.Q, Q + t0 * a.q_row, a.q_row, nq, a.dk, vec);
-            load_transposed<T, DKP>(S.K, K + t0 * a.k_row, a.k_row, nq, a.dk, vec);
+            odd = load_transposed<T, DKP>(S.K, K + t0 * a.k_row, a.k_row, nq, a.dk, vec);
 #pragma unroll
             for (int k = 0; k < kC * kVt / 4 / kThr; ++k) {
                 const int it = t + k * kThr, tok = it / (kVt / 4), c4 = 4 * (it % (kVt / 4));
-                *reinterpret_cast<float4 *>(&S.V[tok][c4]) =
-                    tok < nq ? ld4<T>(V + (t0 + tok) * a.v_row, v0 + c4, a.dv, vec)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v = tok < nq ? ld4<T>(V + (t0 + tok) * a.v_row, v0 + c4, a.dv, vec)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(&S.V[tok][c4]) = v;
+                odd = odd || !all_finite(v);
             }
             if (kFull) {
 #pragma unroll
@@ -247,7 +257,13 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
                 chunk_decays<T>(p, a, b, h, t0, nq, S.gh, S.gl, S.rowf, S.colw, &S.decay,
                                 &S.decay_log2_h, &S.decay_log2_l);
         }
-        __syncthreads();
+        // A pair without a weight (a later token, one before a reset) does not count, and
+        // zero times a value that is not finite would: such a chunk skips those pairs.
+        odd = __syncthreads_or(odd) != 0;
+        auto exponent = [&](int i0, int j0) {  // log2 of the pair's weight
+            const float d = (S.gh[i0] - S.gh[j0]) + (S.gl[i0] - S.gl[j0]);
+            return a.reverse ? -d : d;
+        };
         float4 acc[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -272,9 +288,8 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
                     for (int cc = 0; cc < 4; ++cc) {
                         const int j0 = 4 * tx + cc;
                         const bool in = (a.reverse ? j0 >= i0 : j0 <= i0) && i0 < nq && j0 < nq;
-                        float d = (S.gh[i0] - S.gh[j0]) + (S.gl[i0] - S.gl[j0]);
-                        d = a.reverse ? -d : d;
-                        w[cc][r] = in ? av[cc] * (a.p_scale * ex2_approx(d)) : 0.f;
+                        const float e = ex2_approx(exponent(i0, j0));
+                        w[cc][r] = in && e != 0.f ? av[cc] * (a.p_scale * e) : 0.f;
                     }
                 }
 #pragma unroll
@@ -309,8 +324,19 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
                 st[r] = dec == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                                    : make_float4(st[r].x * dec, st[r].y * dec, st[r].z * dec,
                                                  st[r].w * dec);
+            if (odd) {
+#pragma unroll 1
+                for (int j = 0; j < kC; ++j) {
+                    const float w = S.colw[j];
+                    if (w == 0.f) continue;
+                    float4 v4 = *reinterpret_cast<const float4 *>(&S.V[j][4 * tx]);
+                    v4 = make_float4(v4.x * w, v4.y * w, v4.z * w, v4.w * w);
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) fma4(st[r], S.K[ty + 16 * r][j], v4);
+                }
+            }
 #pragma unroll 2
-            for (int j = 0; j < kC; j += 4) {
+            for (int j = odd ? kC : 0; j < kC; j += 4) {
                 const float4 w4 = *reinterpret_cast<const float4 *>(&S.colw[j]);
                 float4 v4[4];
 #pragma unroll
@@ -334,8 +360,20 @@ __global__ void __launch_bounds__(kThr) linattn_sweep_kernel(const __grid_consta
         if (!kFull) continue;
         __syncthreads();  // P is whole
         if (nq > 0) {
+            if (odd) {
+#pragma unroll 1
+                for (int j = 0; j < kC; ++j) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(&S.V[j][4 * tx]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int i0 = 4 * ty + r;
+                        if ((a.reverse ? j >= i0 : j <= i0) && ex2_approx(exponent(i0, j)) != 0.f)
+                            fma4(acc[r], S.P[j][i0], v4);
+                    }
+                }
+            }
 #pragma unroll 4
-            for (int j = 0; j < kC; ++j) {
+            for (int j = odd ? kC : 0; j < kC; ++j) {
                 const float4 p4 = *reinterpret_cast<const float4 *>(&S.P[j][4 * ty]);
                 const float4 v4 = *reinterpret_cast<const float4 *>(&S.V[j][4 * tx]);
                 fma4(acc[0], p4.x, v4);

@@ -317,8 +317,7 @@ __device__ __forceinline__ void score_weights(const float (&v)[32], const float 
 // zero, a reset, Ye does not count whatever it is). The accumulators are given
 // back (`done`) as soon as the last is read. The outputs go into the staging rows
 // (kF32: to float32 rows in memory, nl of them of dv columns), and with kDot
-// their products with the dot operand, summed over the columns, into `red`. Rows
-// behind the sequence's length come out zero (their operands are zero). In
+// their products with the dot operand, summed over the columns, into `red`. In
 // fragments, so that the transposition to token rows is stmatrix's, and a sum
 // over 32 columns is four additions and a ninth of a shuffle per token (with a
 // lane per column a chunk took 720 instructions and 6000 clocks with the dot
@@ -404,6 +403,23 @@ __device__ __forceinline__ void output_rows(uint32_t t_y, uint32_t t_ye, bf16 *o
             }
             red[32 * th + 8 * (r >> 1) + c2 + (r & 1)] = acc[0];
         }
+    }
+}
+
+// Zeros in a chunk's output rows from nq on (they came out as the state's products with
+// zero operands, NaN where it is not finite): a lane per column of the warp's 32, in the
+// staging rows or, `y` given, in nl float32 rows of dv columns in memory. Out of line:
+// only a row's last chunk comes here.
+__device__ __noinline__ void clear_rows(bf16 *out, int d0, int nq, float *y, long long y_row, int nl,
+                                        int dv) {
+    const int d = d0 + (threadIdx.x & 31);
+    __syncwarp();
+    for (int j = nq; j < kC; ++j) {
+        if (!y)
+            *reinterpret_cast<bf16 *>(reinterpret_cast<char *>(out) + tile_off(j, d)) =
+                __float2bfloat16_rn(0.f);
+        else if (j < nl && d < dv)
+            y[j * y_row + d] = 0.f;
     }
 }
 
@@ -985,6 +1001,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     } else {
                         rows(No(), No());
                     }
+                    if (nq < kC && len < p.seqlen) clear_rows(S.out, d0, nq, yf, y_row, nl, a.dv);
                 } else {
                     arrive(&S.o_empty);
                 }

@@ -132,7 +132,7 @@ def test_gradients_on_the_other_side_of_a_value(dtype, L, dim, strength, heads):
                 assert torch.equal(g[n][:, t + 1:], g0[n][:, t + 1:]), (name, n, t)
 
 
-@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("L,dim", [(150, 64), (150, 128), (2100, 64)])
 def test_rows_behind_a_length_stay_zero(dtype, L, dim):
     """y and gradients of tokens behind a row's length are zero whatever the states

@@ -44,6 +44,8 @@
 
 #include <algorithm>
 
+#include <math_constants.h>
+
 namespace selscan {
 namespace {
 
@@ -122,6 +124,27 @@ __device__ __forceinline__ void stmatrix_t(void *row, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// Two floats at a time: half the instructions, of which the roles' loops have more than
+// the instruction caches like.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // 4 columns of this thread's lane (completed by tmem_st_wait).
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
@@ -237,6 +260,36 @@ template <int D, bool kBwd, bool kFull> struct Cols {
                   "tensor memory");
 };
 
+// What is special about a chunk.
+struct __align__(8) Kind {
+    unsigned char strong;  // the factors of P leave float32's comfortable range
+    unsigned char none[3];
+    unsigned char odd[4];  // V holds a value that is not finite, by 32 columns
+};
+// A chunk's resets, tokens whose factor the exponentials flush to zero, as bits: the
+// first token that token r still sees forward in time, and the one after the last that
+// it sees backwards.
+constexpr double kCutLog2 = -126.0;
+__device__ __forceinline__ int after_cut(uint64_t cuts, int r) {
+    const uint64_t upto = cuts & (~0ull >> (63 - r));
+    return upto ? 63 - __clzll(upto) : 0;
+}
+__device__ __forceinline__ int before_cut(uint64_t cuts, int r) {
+    const uint64_t from = r < 63 ? cuts >> (r + 1) : 0;
+    return from ? r + __ffsll(from) : 64;
+}
+// Bit n to bit 2·n.
+__device__ __forceinline__ uint64_t spread(uint32_t bits) {
+    uint64_t out = 0;
+    for (; bits; bits &= bits - 1) out |= 1ull << 2 * (__ffs(bits) - 1);
+    return out;
+}
+// Rows [*from, *to) of a chunk that the state leaving takes.
+__device__ __forceinline__ void kept_rows(uint64_t cuts, bool rev, int *from, int *to) {
+    *from = rev ? 0 : after_cut(cuts, 63);
+    *to = rev && cuts ? __ffsll(cuts) - 1 : 64;
+}
+
 template <int D, bool kBwd, bool kFull> struct TcSmem {
     static constexpr int kTiles = !kFull ? 2 : kBwd ? 4 : 3;  // (q,) k, v (, dot)
     static constexpr int kK = kFull ? 1 : 0, kV = kK + 1;     // places of k and v
@@ -250,32 +303,25 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     float colf[kSlots][kC];         // column factors of P; in a strong chunk those of A's rounding
     float colw[kSlots][kC];
     float decay[kSlots];
-    int strong[kSlots];             // the factors of P leave float32's comfortable range
+    Kind kind[kSlots];
+    uint64_t cuts[kSlots];          // of strong chunks; others have none
+    uint64_t reached[kFull ? D : 1];  // an odd chunk's tokens that such values reach, by column
+    int odds[4];                    // chunks that were odd, by 32 columns
     float red[4][kC];
     uint64_t full[kStages], empty[kStages], factors[kSlots];
     uint64_t vp_full[2], vp_empty[2], u_full[2], u_empty[2];
     uint64_t s_full, s_empty, p_full, p_empty, st_full, st_empty;
     uint64_t o_full, o_empty, drain;
+    uint64_t odd_read[4];           // the last odd chunk's `reached` is read, by 32 columns
     uint64_t ye_read[4];            // VpOnYe: the strong chunks' outputs are read, in turn
     uint64_t v_sync[2], o_sync;     // the warps of c ◦ V, the output warps
     uint32_t tmem;
     int abort;
 };
 
-// Two floats at a time.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // 32 columns of a row of P as packed bfloat16: scores times f_j (kRow: times
 // `row` too); in a strong chunk times row·f_j·2^(a − A_j). Zero outside columns
-// lo .. hi. Selects, not branches.
+// lo .. hi, whatever the score. Selects, not branches.
 template <bool kRow, bool kStrong>
 __device__ __forceinline__ void score_weights(const float (&v)[32], const float *f, const float *A,
                                               float row, float a, int lo, int hi,
@@ -283,29 +329,21 @@ __device__ __forceinline__ void score_weights(const float (&v)[32], const float 
 #pragma unroll
     for (int e4 = 0; e4 < 8; ++e4) {
         const float4 f4 = *reinterpret_cast<const float4 *>(f + 4 * e4);
-        float x[4];
+        float h[4] = {}, x[4];
         if (kStrong) {
             const float4 h4 = *reinterpret_cast<const float4 *>(A + 4 * e4);
-            const float h[4] = {h4.x, h4.y, h4.z, h4.w};
+            h[0] = h4.x; h[1] = h4.y; h[2] = h4.z; h[3] = h4.w;
+        }
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int j = 4 * e4 + e;
-                float2 w = make_float2(ex2_approx(a - h[e]), ex2_approx(a - h[e + 1]));
-                w = mul2(mul2(w, e ? make_float2(f4.z, f4.w) : make_float2(f4.x, f4.y)),
-                         mul2(make_float2(row, row), make_float2(v[j], v[j + 1])));
-                x[e] = j >= lo && j <= hi ? w.x : 0.f;
-                x[e + 1] = j + 1 >= lo && j + 1 <= hi ? w.y : 0.f;
-            }
-        } else {
-            const float g[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 4 * e4 + e;
-                float w = g[e];
-                if (kRow) w *= row;
-                w *= v[j];
-                x[e] = j >= lo && j <= hi ? w : 0.f;
-            }
+        for (int e = 0; e < 4; e += 2) {
+            const int j = 4 * e4 + e;
+            uint64_t w = e ? pair(f4.z, f4.w) : pair(f4.x, f4.y);
+            if (kStrong) w = mul2(w, pair(ex2_approx(a - h[e]), ex2_approx(a - h[e + 1])));
+            if (kRow || kStrong) w = mul2(w, pair(row, row));
+            w = mul2(w, pair(v[j], v[j + 1]));
+            unpair(w, x[e], x[e + 1]);
+            x[e] = j >= lo && j <= hi ? x[e] : 0.f;
+            x[e + 1] = j + 1 >= lo && j + 1 <= hi ? x[e + 1] : 0.f;
         }
         out[2 * e4] = pack_bf16x2(x[0], x[1]);
         out[2 * e4 + 1] = pack_bf16x2(x[2], x[3]);
@@ -343,14 +381,19 @@ __device__ __forceinline__ void output_rows(uint32_t t_y, uint32_t t_ye, bf16 *o
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float2 f = *reinterpret_cast<const float2 *>(rowf + 32 * th + 8 * c + c2);
+                const uint64_t f2 = pair(f.x, f.y);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float g = k & 1 ? f.y : f.x;
-                    float &x = v[hh][4 * c + k];
-                    if (!kTwo)
-                        x *= g;
-                    else if (!kReset || g != 0.f)
-                        x = fmaf(g, ye[4 * c + k], x);
+                for (int k = 0; k < 4; k += 2) {
+                    float *x = v[hh] + 4 * c + k;
+                    if (!kTwo) {
+                        unpair(mul2(pair(x[0], x[1]), f2), x[0], x[1]);
+                    } else if (!kReset) {
+                        unpair(fma2(f2, pair(ye[4 * c + k], ye[4 * c + k + 1]), pair(x[0], x[1])),
+                               x[0], x[1]);
+                    } else {
+                        if (f.x != 0.f) x[0] = fmaf(f.x, ye[4 * c + k], x[0]);
+                        if (f.y != 0.f) x[1] = fmaf(f.y, ye[4 * c + k + 1], x[1]);
+                    }
                 }
             }
         }
@@ -406,21 +449,179 @@ __device__ __forceinline__ void output_rows(uint32_t t_y, uint32_t t_ye, bf16 *o
     }
 }
 
-// Zeros in a chunk's output rows from nq on (they came out as the state's products with
-// zero operands, NaN where it is not finite): a lane per column of the warp's 32, in the
-// staging rows or, `y` given, in nl float32 rows of dv columns in memory. Out of line:
-// only a row's last chunk comes here.
-__device__ __noinline__ void clear_rows(bf16 *out, int d0, int nq, float *y, long long y_row, int nl,
-                                        int dv) {
-    const int d = d0 + (threadIdx.x & 31);
-    __syncwarp();
-    for (int j = nq; j < kC; ++j) {
-        if (!y)
-            *reinterpret_cast<bf16 *>(reinterpret_cast<char *>(out) + tile_off(j, d)) =
-                __float2bfloat16_rn(0.f);
-        else if (j < nl && d < dv)
-            y[j * y_row + d] = 0.f;
+// ---- values that are not finite ------------------------------------------------------
+// The products run over pairs that do not count (a later token, one that a reset cuts
+// off) with a weight of zero, and zero times a value that is not finite would. So such
+// values leave the operands, and what they do reach is marked by hand. Out of line, and
+// only for the chunks that need it.
+
+// v·0 + sums, pairs of bfloat16: stays zero while every v is finite.
+__device__ __forceinline__ void add_odd(uint32_t &sums, uint32_t v) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sums) : "r"(v), "r"(0u));
+}
+__device__ __forceinline__ bool holds_odd(uint32_t sums) { return (sums & 0x7FFF7FFFu) != 0; }
+
+// c ◦ V of 32 tokens × 16 columns as bfloat16 parts. kOdd: V may be infinite, which the
+// first part takes alone, and counts in rows [from, to) only.
+template <bool kOdd>
+__device__ __forceinline__ void cv_parts(const char *tile, const float *w, int th, int hh, int d0,
+                                         int nvp, int from, int to, uint32_t (&part)[3][8],
+                                         uint32_t &odd) {
+    const int lane = threadIdx.x & 31, r8 = lane >> 4, c2 = 2 * (lane & 3);
+#pragma unroll
+    for (int cp = 0; cp < 2; ++cp) {
+        uint32_t v[4];
+        ldmatrix_t(tile + tile_off(32 * th + 16 * cp + 8 * r8 + (lane & 7), d0 + 16 * hh + (lane & 8)),
+                   v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = 32 * th + 16 * cp + 8 * (k >> 1) + c2;
+            const float2 f = *reinterpret_cast<const float2 *>(w + j);
+            float x0, x1;
+            unpair(mul2(pair(f.x, f.y), pair(bf_lo(v[k]), bf_hi(v[k]))), x0, x1);
+            if (kOdd) {
+                x0 = j >= from && j < to ? x0 : 0.f;
+                x1 = j + 1 >= from && j + 1 < to ? x1 : 0.f;
+            } else {
+                add_odd(odd, v[k]);
+            }
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                if (e >= nvp) break;
+                // all parts but the last by truncation (no conversion)
+                const uint32_t u =
+                    e + 1 < nvp ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
+                                : pack_bf16x2(x0, x1);
+                part[e][4 * cp + k] = u;
+                const bool odd0 = kOdd && !(fabsf(x0) < CUDART_INF_F),
+                           odd1 = kOdd && !(fabsf(x1) < CUDART_INF_F);
+                unpair(fma2(pair(bf_lo(u), bf_hi(u)), pair(-1.f, -1.f), pair(x0, x1)), x0, x1);
+                if (odd0) x0 = 0.f;
+                if (odd1) x1 = 0.f;
+            }
+        }
     }
+}
+
+// The end of c ◦ V for a strong chunk or, by every warp that meets one in V, with values
+// that are not finite. False where a wait gave up.
+//   K: rows that the state leaving does not take are cleared where they hold such a
+//     value, once the chunk's scores have been made of them. The 128 threads of c ◦ V
+//     share the rows.
+//   V (`odd`: this lane met one): c ◦ V of the warp's 32 columns again; in the full pass
+//     such values then leave V, and the tokens that they reach are marked.
+template <int D, bool kBwd, bool kFull>
+__device__ __noinline__ bool odd_chunk(TcSmem<D, kBwd, kFull> &S, int i, bool rev, bool fine,
+                                       bool odd) {
+    typedef TcSmem<D, kBwd, kFull> Smem;
+    typedef Cols<D, kBwd, kFull> C;
+    const int s = i % Smem::kStages, sl = i % Smem::kSlots, lane = threadIdx.x & 31;
+    const int tg = threadIdx.x & 127, g = tg >> 5, d0 = 32 * g;
+    auto wait = [&](uint64_t *bar, int parity) -> bool {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity & 1, &S.abort));
+    };
+    const uint64_t cuts = S.kind[sl].strong ? S.cuts[sl] : 0;
+    int from, to;
+    kept_rows(cuts, rev, &from, &to);
+    if (cuts) {
+        char *tile = reinterpret_cast<char *>(S.tile[s][Smem::kK]);
+        uint32_t sums[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int it = 0; it < D / 16; ++it) {
+            const int e = tg + 128 * it, j = e / (D / 8);
+            uint4 u = *reinterpret_cast<const uint4 *>(tile + tile_off(j, 8 * (e % (D / 8))));
+            if (j >= from && j < to) u = make_uint4(0, 0, 0, 0);
+            add_odd(sums[0], u.x);
+            add_odd(sums[1], u.y);
+            add_odd(sums[2], u.z);
+            add_odd(sums[3], u.w);
+        }
+        const bool found = holds_odd(sums[0] | sums[1] | sums[2] | sums[3]);
+        if (__any_sync(0xffffffffu, found)) {
+            if (kFull && !wait(&S.s_full, i)) return false;
+#pragma unroll 1
+            for (int e = tg; found && e < kC * (D / 8); e += 128) {
+                const int j = e / (D / 8);
+                if (j < from || j >= to)
+                    *reinterpret_cast<uint4 *>(tile + tile_off(j, 8 * (e % (D / 8)))) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+    }
+    if (d0 >= D || !__any_sync(0xffffffffu, odd)) return true;
+    char *tile = reinterpret_cast<char *>(S.tile[s][Smem::kV]);
+    const int nvp = C::vp_parts(fine);
+    const uint32_t taddr = S.tmem + ((uint32_t)d0 << 16);
+    tmem_st_wait();  // the same places are written again
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const int th = q >> 1, hh = q & 1;
+        uint32_t part[3][8], none = 0;
+        cv_parts<true>(tile, S.colw[sl], th, hh, d0, nvp, from, to, part, none);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < nvp)
+                tmem_st_frag(taddr + ((uint32_t)(16 * hh) << 16) + C::vp(i % C::VpBufs, e) + 16 * th,
+                             part[e]);
+    }
+    if (!kFull) return true;
+    const int before = S.odds[g];
+    // the last odd chunk's outputs have read `reached` (and every lane the tile)
+    if (before > 0 && !wait(&S.odd_read[g], before - 1)) return false;
+    __syncwarp();
+    const int d = d0 + lane;
+    uint64_t reached = 0;
+    bool hit = false;
+    for (int k = 0; k < kC; ++k) {
+        const int j = rev ? kC - 1 - k : k;
+        const bool cut = cuts >> j & 1;
+        unsigned short *at = reinterpret_cast<unsigned short *>(tile + tile_off(j, d));
+        if (!rev && cut) hit = false;
+        if ((*at & 0x7F80) == 0x7F80) {
+            *at = 0;
+            hit = true;
+        }
+        if (hit) reached |= 1ull << j;
+        if (rev && cut) hit = false;
+    }
+    S.reached[d] = reached;
+    if (lane == 0) {
+        S.odds[g] = before + 1;
+        S.kind[sl].odd[g] = 1;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    return true;
+}
+
+// A chunk's output rows put right after output_rows: the tokens that values reach which
+// are not finite become NaN, rows from nq on zero (they came out as the state's products
+// with zero operands). A lane per column of the warp's 32, in the staging rows or in the
+// float32 rows in memory.
+template <int D, bool kBwd, bool kFull>
+__device__ __noinline__ void odd_rows(TcSmem<D, kBwd, kFull> &S, const LinattnParams &p,
+                                      const SweepArgs &a, int b, int h, int len, int t0, bool odd) {
+    const int lane = threadIdx.x & 31, g = (threadIdx.x >> 5) & 3, d = 32 * g + lane;
+    const int nq = min(kC, len - t0), nl = (int)min((long long)kC, p.seqlen - t0);
+    float *y = kBwd && a.y_f32 ? static_cast<float *>(a.y) +
+                                     (((long long)b * p.seqlen + t0) * p.heads + h) * a.dv
+                               : nullptr;
+    const uint64_t reached = odd ? S.reached[d] : 0;
+    __syncwarp();
+    for (int j = 0; j < kC; ++j) {
+        const bool nan = j < nq && ((reached >> j) & 1);
+        if (kBwd && __any_sync(0xffffffffu, nan) && lane == 0) S.red[g][j] = CUDART_NAN_F;
+        if (!nan && j < nq) continue;
+        if (!y)
+            *reinterpret_cast<unsigned short *>(reinterpret_cast<char *>(S.out) + tile_off(j, d)) =
+                nan ? 0x7FFF : 0;
+        else if (j < nl && d < a.dv)
+            y[(long long)j * p.heads * a.dv + d] = nan ? CUDART_NAN_F : 0.f;
+    }
+    __syncwarp();
+    if (odd && lane == 0) mbar_arrive(&S.odd_read[g]);
 }
 
 // One block: one (sweep, batch row, head, segment). kFull false: only the
@@ -479,7 +680,11 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         mbar_init(&S.drain, 1);
         mbar_init(&S.o_full, 1);
         mbar_init(&S.o_empty, 4);
-        for (int k = 0; k < 4; ++k) mbar_init(&S.ye_read[k], 4);
+        for (int k = 0; k < 4; ++k) {
+            mbar_init(&S.ye_read[k], 4);
+            mbar_init(&S.odd_read[k], 1);
+            S.odds[k] = 0;
+        }
         mbar_init(&S.o_sync, 4);
         S.abort = 0;
         fence_barrier_init();
@@ -573,13 +778,17 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     colf[e] = a.col_scale * ex2_approx(-A[e]);
                     colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
                 }
-                far = __any_sync(0xffffffffu, far);
+                // the total too: a reset on a chunk's first token is in no A backwards
+                far = __any_sync(0xffffffffu, far || !(fabsf((float)end) <= kRange));
                 if (far) {
                     // A strong chunk's weights are 2^(A_row − A_col) from A as it is rounded
                     // (a step of 2^-10 behind many resets, where it passes 2^13; the
                     // difference itself is exact there) and the factors of what it lost.
                     colf[0] = ex2_approx((float)((double)A[0] - exact[0]));
                     colf[1] = ex2_approx((float)((double)A[1] - exact[1]));
+                    const uint32_t cut0 = __ballot_sync(0xffffffffu, g0 < kCutLog2),
+                                   cut1 = __ballot_sync(0xffffffffu, g1 < kCutLog2);
+                    if (lane == 0) S.cuts[i % kSlots] = spread(cut0) | spread(cut1) << 1;
                 }
                 const int sl = i % kSlots;
                 *reinterpret_cast<float2 *>(&S.A[sl][2 * lane]) = make_float2(A[0], A[1]);
@@ -588,7 +797,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) = make_float2(colw[0], colw[1]);
                 if (lane == 0) {
                     S.decay[sl] = ex2_approx((float)end);
-                    S.strong[sl] = far;
+                    *reinterpret_cast<uint2 *>(&S.kind[sl]) = make_uint2(far, 0);
                 }
                 seg_log2 += end;
                 arrive(&S.full[s]);
@@ -605,7 +814,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             // ---- MMA issuer ---------------------------------------------------------------
             // The warp waits (a lane per barrier, so that several waits cost one), an elected
             // lane issues. Descriptors are a tile's first plus an offset in 16-byte units:
-            // an MMA of 64 columns is bound by its issue (about 50 clocks).
+            // an MMA of 64 columns is bound by its issue (about 50 clocks), so that its
+            // loops can be rolled for the instruction caches' sake (2 × 4096 tokens of 32
+            // heads of 128: 130 → 121 µs).
             constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);   // Q (K-major), K (K-major)
             constexpr uint32_t id_yi = idesc_bf16(128, 64, 1, 0);  // Vᵀ (M-major), P (K-major)
             constexpr uint32_t id_ye = idesc_bf16(128, 64, 0, 0);  // S (tensor memory), Q
@@ -634,7 +845,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                                k = umma_desc_sw128(smem_addr(S.tile[s][Smem::kK]), 16, 1024);
                 if (!wait2(&S.full[s], i / kStages, &S.s_empty, (i & 1) ^ 1)) return;
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < D / 16; ++x)
                         umma_bf16(tmem + C::S, q + kstep(x), k + kstep(x), id_s, x > 0);
                     umma_commit(&S.s_full);
@@ -653,7 +864,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         if (part >= nvp) break;
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < kC / 16; ++x)
                             umma_bf16_ts(u, tmem + C::vp(vb, part) + x * 8, k + x * kTok,
                                          id_u, part > 0 || x > 0);
@@ -671,7 +882,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 }
                 // Ye = S_inᵀ Qᵀ and Yi = Vᵀ Pᵀ, the second on top of the first where the row
                 // factors stand in the outputs
-                const bool two = kBwd || S.strong[i % kSlots] != 0;
+                const bool two = kBwd || S.kind[i % kSlots].strong != 0;
                 const uint32_t yi = tmem + C::Yi, ye = two ? tmem + C::Ye : yi;
                 const uint64_t q = umma_desc_sw128(smem_addr(S.tile[s][0]), 16, 1024);
                 const uint64_t v = umma_desc_sw128(smem_addr(S.tile[s][Smem::kV]), kSlab, 1024),
@@ -682,12 +893,12 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (elect_one()) {
 #pragma unroll
                     for (int part = 0; part < (int)C::StParts; ++part)
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < D / 16; ++x)
                             umma_bf16_ts(ye, tmem + C::St + part * (D / 2) + x * 8, q + kstep(x), id_ye,
                                          part > 0 || x > 0);
                     umma_commit(&S.st_empty);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < kC / 16; ++x)
                         umma_bf16(yi, v + x * kTok, pp + kstep(x), id_yi, !two || x > 0);
                     umma_commit(&S.o_full);
@@ -710,14 +921,22 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 const int r = 32 * warp + lane;
                 for (int i = 0; i < n; ++i) {
                     const int nq = min(kC, len - chunk_of(i) * kC), sl = i % kSlots;
-                    ok = wait(&S.factors[sl], i / kSlots) && wait(&S.s_full, i);
+                    ok = wait(&S.factors[sl], i / kSlots);
                     if (!ok) break;
-                    tc_fence_after();
-                    const bool strong = S.strong[sl] != 0;
+                    const bool strong = S.kind[sl].strong != 0;
                     const float rf = S.rowf[sl][r], ar = S.A[sl][r];
                     // in a strong chunk: the reciprocal of a factor within 2^-11.5 of one, to 2^-23
                     const float low = a.p_scale * (2.f - S.colf[sl][r]);
-                    const int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
+                    int lo = rev ? r : 0, hi = r >= nq ? -1 : rev ? nq - 1 : r;
+                    if (strong) {  // what stands beyond a reset does not count
+                        if (rev)
+                            hi = min(hi, before_cut(S.cuts[sl], r) - 1);
+                        else
+                            lo = after_cut(S.cuts[sl], r);
+                    }
+                    ok = wait(&S.s_full, i);
+                    if (!ok) break;
+                    tc_fence_after();
                     char *row = reinterpret_cast<char *>(S.P) + r * 128;
                     uint32_t out[16];
                     auto block = [&](int half, bool last) {
@@ -767,7 +986,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         // ---- c ◦ V as bfloat16 parts, column d of V on lane d --------------------------
         // In the pass over the segments' own states the output warps take every other chunk.
         const int group = warp >= 16 ? 1 : 0, tg = t - (group ? 512 : 128);
-        const int d0 = 32 * (warp & 3), r8 = lane >> 4, c2 = 2 * (lane & 3);
+        const int d0 = 32 * (warp & 3);
         uint32_t syncs = 0;
         int strongs = 0;
         for (int i = group; i < n; i += kFull ? 1 : 2) {
@@ -790,40 +1009,17 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (!ok) break;
             }
             const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
-            const float *w = S.colw[i % kSlots];
+            const int sl = i % kSlots;
+            const float *w = S.colw[sl];
+            const bool strong = S.kind[sl].strong != 0;
+            uint32_t odd = 0;  // NaN where V is not finite
             // rolled: the loop bodies of the five roles share the instruction caches. The
             // first quarter is made while U still reads the previous parts.
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {  // 32 tokens × 16 columns
                 const int th = q >> 1, hh = q & 1;
                 uint32_t part[3][8];
-                if (d0 < D) {
-#pragma unroll
-                    for (int cp = 0; cp < 2; ++cp) {
-                        uint32_t v[4];
-                        ldmatrix_t(tile + tile_off(32 * th + 16 * cp + 8 * r8 + (lane & 7),
-                                                   d0 + 16 * hh + (lane & 8)),
-                                   v);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = *reinterpret_cast<const float2 *>(
-                                w + 32 * th + 16 * cp + 8 * (k >> 1) + c2);
-                            float x0 = f.x * bf_lo(v[k]), x1 = f.y * bf_hi(v[k]);
-#pragma unroll
-                            for (int e = 0; e < 3; ++e) {
-                                if (e >= nvp) break;
-                                // all parts but the last by truncation (no conversion)
-                                const uint32_t u =
-                                    e + 1 < nvp
-                                        ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632)
-                                        : pack_bf16x2(x0, x1);
-                                part[e][4 * cp + k] = u;
-                                x0 -= bf_lo(u);
-                                x1 -= bf_hi(u);
-                            }
-                        }
-                    }
-                }
+                if (d0 < D) cv_parts<false>(tile, w, th, hh, d0, nvp, 0, kC, part, odd);
                 if (q == 0 && use > 0) {
                     // U has read what stands there
                     ok = wait(kVBufs == kUBufs ? &S.u_full[vb] : &S.vp_empty[vb], use - 1);
@@ -840,8 +1036,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     // outputs of chunk i − 4 are: o_empty could be two phases behind, one of
                     // four barriers that strong chunks take in turn is one behind at most.
                     const int before = strongs;
-                    strongs += (S.strong[(i - 1) % kSlots] != 0) +
-                               (i > 1 && S.strong[(i - 2) % kSlots] != 0);
+                    strongs += (S.kind[(i - 1) % kSlots].strong != 0) +
+                               (i > 1 && S.kind[(i - 2) % kSlots].strong != 0);
                     if (strongs > before) {
                         ok = wait(&S.ye_read[(strongs - 1) & 3], (strongs - 1) >> 2);
                         if (!ok) break;
@@ -858,6 +1054,10 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 }
             }
             if (!ok) break;
+            if (__any_sync(0xffffffffu, strong || holds_odd(odd))) {
+                ok = odd_chunk(S, i, rev, fine, holds_odd(odd));
+                if (!ok) break;
+            }
             if (d0 < D) tmem_st_wait();
             tc_fence_before();
             arrive(&S.vp_full[vb]);
@@ -972,15 +1172,18 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                                     : nullptr;
                     const bf16 *dot = S.tile[s][Smem::kTiles - 1];
                     const uint32_t t_y = tmem + lanes + C::Yi, t_ye = tmem + lanes + C::Ye;
+                    const int sl = i % kSlots;
+                    const uint2 kind = *reinterpret_cast<const uint2 *>(&S.kind[sl]);
+                    const bool strong = (kind.x & 0xFF) != 0,
+                               odd = (kind.y >> (8 * (warp & 3)) & 0xFF) != 0;
                     auto done = [&]() {  // the next chunk's products may come
                         tc_fence_before();
                         arrive(&S.o_empty);
-                        if (C::VpOnYe && S.strong[i % kSlots]) arrive(&S.ye_read[strongs++ & 3]);
+                        if (C::VpOnYe && strong) arrive(&S.ye_read[strongs++ & 3]);
                     };
                     auto rows = [&](auto is_f32, auto is_dot) {
                         constexpr bool kF32 = decltype(is_f32)::value, kDot = decltype(is_dot)::value;
-                        const int sl = i % kSlots;
-                        if (S.strong[sl])
+                        if (strong)
                             output_rows<kF32, kDot, true, true>(t_y, t_ye, S.out, dot, S.red[warp & 3],
                                                                 S.rowf[sl], d0, yf, y_row, nl, a.dv,
                                                                 done);
@@ -1001,7 +1204,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     } else {
                         rows(No(), No());
                     }
-                    if (nq < kC && len < p.seqlen) clear_rows(S.out, d0, nq, yf, y_row, nl, a.dv);
+                    if (odd || (nq < kC && len < p.seqlen))
+                        odd_rows(S, p, a, b, h, len, t0, odd);
                 } else {
                     arrive(&S.o_empty);
                 }
@@ -1071,6 +1275,7 @@ template <int D, bool kBwd, bool kFine>
 cudaError_t launch(const LinattnParams &p, const TcMaps &maps, cudaStream_t stream) {
     const int smem = (int)sizeof(TcSmem<D, kBwd, true>) + 1024;
     const int smem_own = (int)sizeof(TcSmem<D, kBwd, false>) + 1024;
+    static_assert(sizeof(TcSmem<D, kBwd, true>) + 1024 <= 232448, "shared memory");
     auto full = linattn_tc_kernel<D, kBwd, true, kFine>;
     auto state = linattn_tc_kernel<D, kBwd, false, kFine>;
     cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

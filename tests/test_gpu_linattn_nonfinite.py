@@ -17,7 +17,7 @@ import selective_state_space_42_b200 as ss
 from test_gpu_linattn import DEV, dev, make
 
 pytestmark = pytest.mark.gpu
-DTYPES = ["f32"]
+DTYPES = ["f32", "bf16"]
 BAD = [math.inf, -math.inf, math.nan]
 
 

@@ -7,7 +7,8 @@ import torch
 
 import selective_state_space_42_b200 as ss
 
-from test_gpu_linattn import DEV, DT, check_fwd, dev, make
+import test_gpu_linattn as t_la
+from test_gpu_linattn import DEV, DT, check_bwd, check_fwd, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,36 @@ def test_large_products_under_decay(dtype):
         i[k] = (i[k].float() * 2.0 ** e).to(i[k].dtype)
     i["g"][:] = -0.5546875
     check_fwd(i, dtype, what="large")
+
+
+def _off(t):
+    """The same values one element behind a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+    out = buf[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "dy", "h0", "dS"])
+@pytest.mark.parametrize("heads", [2, 4])
+def test_gradient_of_rows_off_16_bytes(dtype, name, heads, monkeypatch):
+    """Each operand in turn; heads of their own and shared ones."""
+    i = make(2, 150, 2, heads, 64, 64, dtype, 62, h0=True)
+    real = t_la.dev
+
+    def dev_off(i):
+        d = real(i)
+        d[name] = _off(d[name])
+        return d
+
+    monkeypatch.setattr(t_la, "dev", dev_off)
+    check_bwd(i, dtype, what=f"{name} off")
+    check_fwd(i, dtype, what=f"{name} off")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_a_layer_with_shared_heads_and_a_state(dtype):
+    """Shared heads and a first state together, over segments."""
+    i = make(1, 1500, 2, 4, 128, 128, dtype, 63, h0=True, strength=0.1)
+    check_bwd(i, dtype, what="layer")

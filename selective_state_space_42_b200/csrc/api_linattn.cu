@@ -540,7 +540,7 @@ int selscan_block_norm_fwd(const void *x, const selscan_block_norm_options_t *op
 
 int64_t selscan_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
     if (rows < 1 || rows > 0x7FFFFFFF || dim < 1 || dim > kBnMaxDim) return 0;
-    return (int64_t)block_norm_bwd_blocks(rows, 128) * 2 * dim * (int64_t)sizeof(float);
+    return (int64_t)block_norm_bwd_blocks(rows, (int)dim) * 2 * dim * (int64_t)sizeof(float);
 }
 
 int selscan_block_norm_bwd(const void *x, const selscan_block_norm_options_t *options,

@@ -813,13 +813,19 @@ cudaError_t fwd_typed(const BlockNormParams &p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
 }
 
+int blocks_of(long long rows, int threads) {
+    const long long most = (long long)sm_count() * std::max(2, 1024 / std::max(threads, 128));
+    return (int)std::max<long long>(1, std::min(rows, most));
+}
+
 template <typename T, typename TR, int kVec, int kNV, int kThreads, int kBlocks>
 cudaError_t bwd(const BlockNormParams &params, const Map &m, cudaStream_t stream) {
     BlockNormParams p = params;
     const long long want = (p.rows + m.rows_per - 1) / m.rows_per;
     const int threads = m.row_threads * m.rows_per;
-    long long blocks =
-        std::min<long long>(want, block_norm_bwd_blocks(p.rows, std::max(threads, 128)));
+    // the workspace has room for so many
+    const long long room = block_norm_bwd_blocks(p.rows, p.dim);
+    long long blocks = std::min({want, room, (long long)blocks_of(p.rows, threads)});
     bool ring = false;
     if constexpr (kVec == 8) {
         constexpr int kRoom = kBlocks == 2 ? 100 << 10 : 200 << 10;
@@ -864,11 +870,11 @@ cudaError_t bwd_typed(const BlockNormParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-// Blocks of the gradient, each with its column sums: about a thousand threads
-// an SM, two blocks at least.
-int block_norm_bwd_blocks(long long rows, int threads) {
-    const long long most = 148ll * std::max(2, 1024 / std::max(threads, 1));
-    return (int)std::max<long long>(1, std::min(rows, most));
+// Blocks of the gradient, each with its column sums: about a thousand threads an SM of
+// the fewest that a row of this width gets (8 elements each, up to 512 threads), two
+// blocks at least. 16384 columns: 39 MB of sums (155 if sized for 128 threads).
+int block_norm_bwd_blocks(long long rows, int dim) {
+    return blocks_of(rows, std::min((dim + 7) / 8, 512));
 }
 
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream) {

@@ -33,7 +33,7 @@ struct BlockNormParams {
 };
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool bf16, cudaStream_t stream);
-// Sizes `partial` (threads a block: 128 at least).
-int block_norm_bwd_blocks(long long rows, int threads);
+// Sizes `partial`.
+int block_norm_bwd_blocks(long long rows, int dim);
 
 }  // namespace selscan

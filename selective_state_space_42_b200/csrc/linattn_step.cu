@@ -9,6 +9,7 @@
 // two an SM: the columns are split over up to four blocks, which shortens the
 // latency of a small batch's call. 256 rows of 32 heads of 128 × 128: 162 µs, the
 // copy rate of HBM; one row: 2.5 µs.
+#include "api_util.cuh"
 #include "linattn_params.cuh"
 
 namespace selscan {
@@ -138,7 +139,7 @@ cudaError_t launch_typed(const LinattnStepParams &p, cudaStream_t stream) {
     if (!vec) {
         linattn_step_kernel<T>
             <<<dim3((unsigned)pairs, (unsigned)((p.dv + 31) / 32)), kThr, 0, stream>>>(p);
-    } else if (p.dv <= 32 || pairs < 296) {
+    } else if (p.dv <= 32 || pairs < 2ll * sm_count()) {
         linattn_step_vec_kernel<T, 8>
             <<<dim3((unsigned)pairs, (unsigned)((p.dv + 31) / 32)), kThr, 0, stream>>>(p);
     } else if (p.dv <= 64) {

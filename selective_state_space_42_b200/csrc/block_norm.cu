@@ -14,10 +14,10 @@
 // time, or on several where a row needs no more than a warp: thread t holds
 // kNV vectors of kVec elements of its group's columns, so that sums over a
 // group stay within its threads. All arithmetic and all sums are float32; the
-// only roundings to bfloat16 are the stores. 16384 rows of 5120 in bfloat16: 177 µs,
-// 73% of the HBM copy rate (the instructions' issue is at 75%); the gradient of 16384
-// rows of 2560, 287 µs, 50%: its column sums and operands take 96 registers a thread,
-// which leaves 20 warps an SM to hide two barriers a row.
+// only roundings to bfloat16 are the stores. 16384 rows of 5120 in bfloat16: 187 µs,
+// 70% of the HBM copy rate (the instructions' issue is at 75%); the gradient of 16384
+// rows of 2560, 286 µs, 50%: its column sums and operands take 96 registers a thread and
+// 100 bytes of spills, which leaves 20 warps an SM to hide two barriers a row.
 #include "block_norm.cuh"
 #include "tma_util.cuh"
 
@@ -800,6 +800,16 @@ cudaError_t fwd(const BlockNormParams &params, const Map &m, cudaStream_t stream
     return cudaGetLastError();
 }
 
+// The kernel with the fewest elements a thread that covers a row, since the sums and the
+// row itself are registers: vectors of 8 where the rows allow, else single elements. The
+// thread limits are what the registers leave: 640 threads twice an SM at 48 registers
+// (8 elements, up to 5120 columns), 512 to 1024 with more elements else. In the gradient
+// 8 elements take 96 registers: 320 threads twice (up to 2560 columns) or 640 once an SM,
+// and 16 or 32 elements beyond. Its kernels spill: 100 to 330 bytes a thread at 8
+// elements, 0.4 to 1.1 KB at 16, up to 4 KB at 32 (and so do rows of 32 single elements
+// a thread forward, 1.1 KB). Measured, 41.9 M elements of bfloat16 with a float32 residual and all
+// parts, as shares of the copy rate, forward / gradient: 1536 columns 53 / 35%, 2560
+// 68 / 50%, 4096 81 / 40%, 5120 86 / 46%, 8192 55 / 34%.
 template <typename T, typename TR>
 cudaError_t fwd_typed(const BlockNormParams &p, cudaStream_t stream) {
     Map m;

@@ -545,15 +545,22 @@ typedef struct {
  *   final_state   [batch, heads, dk, dv]          float32   NULL -> not written; may be
  *                                                 options->initial_state itself
  *   heads a multiple of qk_heads, 1 <= dk, dv <= 128, batch·heads <= 2^22.
- * A log decay of −∞ (any below −111) resets: what came before that token does
- * not count. Tokens at or behind a row's length are not used: their y is zero
- * and final_state is the state after the row's last token; their k and v may
- * hold anything. Chunks of 64 tokens; float32 state, sums and decays. bfloat16
- * I/O whose rows suit it (dk, dv multiples of 8, 16-byte rows) runs on the
- * tensor cores (tcgen05) with the products' weights and the entering state as
- * bfloat16 operands, the state's own update keeping 24 bits; everything else
- * in float32 on the CUDA cores. Few (batch row, head) pairs: a sequence is cut
- * into segments that run side by side after a pass over their own states.
+ * A log decay of −∞ (any below −87.4, whose factor float32 flushes to zero)
+ * resets: what came before that token does not count, whatever it holds. Tokens
+ * at or behind a row's length are not used: their y is zero and final_state is
+ * the state after the row's last token; their k and v may hold anything.
+ * A value that is not finite reaches y of its token and of later ones up to the
+ * next reset, and the state leaving, as long as float32 holds its weight; one of
+ * v only its own column. What it reaches is infinite or NaN (the state takes an
+ * infinite v as it stands), and nothing else changes.
+ * Chunks of 64 tokens; float32 state, sums and decays. bfloat16 I/O whose rows
+ * suit it (dk, dv multiples of 8, 16-byte rows) runs on the tensor cores
+ * (tcgen05) with the products' weights and the entering state as bfloat16
+ * operands, the state's own update keeping 24 bits; there a chunk's decay stands
+ * between its factors on the way, so that y is finite where the sums of
+ * |scale·(q·k)·v| stay below 2^96. Everything else runs in float32 on the CUDA
+ * cores. Few (batch row, head) pairs: a sequence is cut into segments that run
+ * side by side after a pass over their own states.
  * Workspace (256-byte aligned; NULL: allocated on the stream) of
  * selscan_linattn_workspace_bytes() bytes. Results do not depend on anything
  * but the inputs (fixed summation order). Asynchronous like selscan_fwd.
@@ -585,7 +592,12 @@ SELSCAN_API int64_t selscan_linattn_workspace_bytes(int64_t batch, int64_t seqle
  *                                                 given by head is a constant)
  *   dinitial_state [batch, heads, dk, dv]         float32   NULL -> not written
  * States are recomputed. Every output is overwritten; those of tokens behind a
- * row's length are zero. Options, limits and workspace
+ * row's length are zero. dlog_decay is made as a running sum over the later
+ * tokens, from the next reset back, of q·dq − k·dk: it carries the errors of
+ * these products, which cancel (2^-20 of their size in float32, 2^-17 in
+ * bfloat16), and a value that is not finite makes it so back to the last reset.
+ * The other gradients take such values as the forward does: dq those of earlier
+ * tokens, dk and dv those of later ones. Options, limits and workspace
  * (selscan_linattn_bwd_workspace_bytes()) as for the forward. Outputs are
  * contiguous and overlap no input.
  */

@@ -17,11 +17,13 @@
 // product with q). Too few heads to fill the device: the sequence is cut into
 // segments (LinattnPlan).
 //
-// Bound: the float32 FMA rate; per chunk 2·64·64·(dk + dv) + 2·2·64·dk·dv
-// operations a head, which the products' register tiles (4×4, and
-// (dk/16)×4 for the state) feed from shared memory. With few chunks a block, as on
-// 3 × 1111 tokens of 6 heads 48 → 80 in float32 (96–106 µs, 125 with equal segments
-// after a pass over all their states), the latency of a chunk: 19 µs.
+// Bound: the float32 FMAs, at 8 warps an SM, which register tiles (4×4, and (DKP/16)×4
+// for the state) feed from shared memory. A chunk of a head needs 2·64·64·(dk + dv) +
+// 2·2·64·dk·dv operations; a block executes 2·64·64·(2·dk + DKP + 64) for its 64 value
+// columns, DKP the larger dimension of both rounded up to 64 or 128, and two blocks both
+// make the scores. On 3 × 1111 tokens of 6 heads 48 → 80 in float32 (107 µs; 125 with
+// equal segments after a pass over all their states) that is 4.7 MFLOP a chunk for 2.0,
+// 19 µs, four chunks a block.
 #include "linattn_params.cuh"
 
 #include <algorithm>

@@ -12,7 +12,7 @@
 // A pair's weight exp(A_row − A_col) is split: P takes 1/exp(A_col), the output
 // r = exp(A_row), so that P costs a product per score and the two products one
 // accumulator. The gradient keeps the row factor in P and the products apart: its
-// sweeps for dq and dk must round the same weights the same way (their dot
+// sweeps for dq and dk must make the same weights, to about 2^-20 (their dot
 // products cancel in the log decays' gradient). So does, with an exponential per
 // score, a chunk whose factors leave 2^±32 (a reset, a few tokens of strong decay).
 // Q, K, V (and in the gradient the operand of the dot product) come by TMA into
@@ -35,10 +35,11 @@
 // there c ◦ V has three parts too, the third in the scores' columns.
 //
 // Bound: a chunk's chain of scores, P, output product and store, and of c ◦ V, U and
-// state: 2.7 µs a chunk at D = 128 (3.4 in the gradient, 1.6 in the pass over states)
-// where the MMAs alone take 0.9; 2 × 4096 tokens of 32 heads of 128: 124 µs (1786 on
-// the CUDA cores), 65536 tokens of 16 heads 464 µs. Chunks of 128 tokens would double
-// the work on P, the largest of the roles' shares.
+// state: 2.7 µs a chunk at D = 128 (3.5 in the gradient, 1.7 in the pass over states)
+// where the MMAs alone take 0.9; 2 × 4096 tokens of 32 heads of 128: 121 µs (1786 on
+// the CUDA cores), 65536 tokens of 16 heads 467 µs. Chunks of 128 tokens would double
+// the work on P, the largest of the roles' shares. The full passes at D = 128 spill 160
+// to 190 bytes a thread at their 96 registers.
 #include "linattn_params.cuh"
 #include "umma_util.cuh"
 

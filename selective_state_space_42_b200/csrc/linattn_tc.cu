@@ -265,7 +265,8 @@ template <int D, bool kBwd, bool kFull> struct Cols {
 struct __align__(8) Kind {
     unsigned char strong;  // the factors of P leave float32's comfortable range
     unsigned char none[3];
-    unsigned char odd[4];  // V holds a value that is not finite, by 32 columns
+    unsigned char odd[4];  // bit 0: V holds a value that is not finite, by 32 columns; bit 1:
+                           // the row's length ends in it
 };
 // A chunk's resets, tokens whose factor the exponentials flush to zero, as bits: the
 // first token that token r still sees forward in time, and the one after the last that
@@ -588,41 +589,50 @@ __device__ __noinline__ bool odd_chunk(TcSmem<D, kBwd, kFull> &S, int i, bool re
         if (rev && cut) hit = false;
     }
     S.reached[d] = reached;
+    if (kBwd)  // their dot products too
+        for (int j = 0; j < kC; ++j)
+            if (reached >> j & 1)
+                *reinterpret_cast<unsigned short *>(
+                    reinterpret_cast<char *>(S.tile[s][Smem::kTiles - 1]) + tile_off(j, d)) = 0x7FFF;
     if (lane == 0) {
         S.odds[g] = before + 1;
-        S.kind[sl].odd[g] = 1;
+        S.kind[sl].odd[g] |= 1;
     }
     fence_proxy_async_smem();
     __syncwarp();
     return true;
 }
 
-// A chunk's output rows put right after output_rows: the tokens that values reach which
-// are not finite become NaN, rows from nq on zero (they came out as the state's products
-// with zero operands). A lane per column of the warp's 32, in the staging rows or in the
-// float32 rows in memory.
+// A chunk's output rows put right before they are stored, by the warp that stores: the
+// tokens that values reach which are not finite become NaN, rows behind the row's length
+// zero (they came out as the state's products with zero operands). In the staging rows
+// or in the float32 rows in memory.
 template <int D, bool kBwd, bool kFull>
 __device__ __noinline__ void odd_rows(TcSmem<D, kBwd, kFull> &S, const LinattnParams &p,
-                                      const SweepArgs &a, int b, int h, int len, int t0, bool odd) {
-    const int lane = threadIdx.x & 31, g = (threadIdx.x >> 5) & 3, d = 32 * g + lane;
-    const int nq = min(kC, len - t0), nl = (int)min((long long)kC, p.seqlen - t0);
+                                      const SweepArgs &a, int b, int h, int len, int t0, int sl) {
+    const int lane = threadIdx.x & 31, nq = min(kC, len - t0),
+              nl = (int)min((long long)kC, p.seqlen - t0);
     float *y = kBwd && a.y_f32 ? static_cast<float *>(a.y) +
                                      (((long long)b * p.seqlen + t0) * p.heads + h) * a.dv
                                : nullptr;
-    const uint64_t reached = odd ? S.reached[d] : 0;
-    __syncwarp();
-    for (int j = 0; j < kC; ++j) {
-        const bool nan = j < nq && ((reached >> j) & 1);
-        if (kBwd && __any_sync(0xffffffffu, nan) && lane == 0) S.red[g][j] = CUDART_NAN_F;
-        if (!nan && j < nq) continue;
-        if (!y)
-            *reinterpret_cast<unsigned short *>(reinterpret_cast<char *>(S.out) + tile_off(j, d)) =
-                nan ? 0x7FFF : 0;
-        else if (j < nl && d < a.dv)
-            y[(long long)j * p.heads * a.dv + d] = nan ? CUDART_NAN_F : 0.f;
+    for (int g = 0; g < D / 32; ++g) {
+        const bool odd = S.kind[sl].odd[g] & 1;
+        const int d = 32 * g + lane;
+        const uint64_t reached = odd ? S.reached[d] : 0;
+        for (int j = odd ? 0 : nq; j < kC; ++j) {
+            const bool nan = j < nq && ((reached >> j) & 1);
+            if (!nan && j < nq) continue;
+            if (!y)
+                *reinterpret_cast<unsigned short *>(reinterpret_cast<char *>(S.out) +
+                                                    tile_off(j, d)) = nan ? 0x7FFF : 0;
+            else if (j < nl && d < a.dv)
+                y[(long long)j * p.heads * a.dv + d] = nan ? CUDART_NAN_F : 0.f;
+        }
+        __syncwarp();
+        if (odd && lane == 0) mbar_arrive(&S.odd_read[g]);
     }
+    fence_proxy_async_smem();
     __syncwarp();
-    if (odd && lane == 0) mbar_arrive(&S.odd_read[g]);
 }
 
 // One block: one (sweep, batch row, head, segment). kFull false: only the
@@ -798,7 +808,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 *reinterpret_cast<float2 *>(&S.colw[sl][2 * lane]) = make_float2(colw[0], colw[1]);
                 if (lane == 0) {
                     S.decay[sl] = ex2_approx((float)end);
-                    *reinterpret_cast<uint2 *>(&S.kind[sl]) = make_uint2(far, 0);
+                    *reinterpret_cast<uint2 *>(&S.kind[sl]) =
+                        make_uint2(far, len - t0 < kC && len < p.seqlen ? 0x02020202u : 0u);
                 }
                 seg_log2 += end;
                 arrive(&S.full[s]);
@@ -1174,9 +1185,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     const bf16 *dot = S.tile[s][Smem::kTiles - 1];
                     const uint32_t t_y = tmem + lanes + C::Yi, t_ye = tmem + lanes + C::Ye;
                     const int sl = i % kSlots;
-                    const uint2 kind = *reinterpret_cast<const uint2 *>(&S.kind[sl]);
-                    const bool strong = (kind.x & 0xFF) != 0,
-                               odd = (kind.y >> (8 * (warp & 3)) & 0xFF) != 0;
+                    const bool strong = S.kind[sl].strong != 0;
                     auto done = [&]() {  // the next chunk's products may come
                         tc_fence_before();
                         arrive(&S.o_empty);
@@ -1205,8 +1214,6 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                     } else {
                         rows(No(), No());
                     }
-                    if (odd || (nq < kC && len < p.seqlen))
-                        odd_rows(S, p, a, b, h, len, t0, odd);
                 } else {
                     arrive(&S.o_empty);
                 }
@@ -1215,6 +1222,8 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 arrive(&S.o_sync);
                 ok = wait(&S.o_sync, syncs++);
                 if (!ok) break;
+                if (warp == 16 && *reinterpret_cast<const uint32_t *>(S.kind[i % kSlots].odd))
+                    odd_rows(S, p, a, b, h, len, t0, i % kSlots);
                 if (tl == 0 && !f32) {
                     for (int c = 0; c < a.dv; c += 64)
                         tma_store_4d(my, S.out + (c >> 6) * (kC * 64), c, h, t0, b);

@@ -11,10 +11,12 @@
 //   y = r ◦ Y,   S ← exp(G_end)·S + U
 // A pair's weight exp(A_row − A_col) is split: P takes 1/exp(A_col), the output
 // r = exp(A_row), so that P costs a product per score and the two products one
-// accumulator. The gradient keeps the row factor in P and the products apart: its
-// sweeps for dq and dk must make the same weights, to about 2^-20 (their dot
-// products cancel in the log decays' gradient). So does, with an exponential per
-// score, a chunk whose factors leave 2^±32 (a reset, a few tokens of strong decay).
+// accumulator; both are taken about the middle of the chunk's decay, the entering
+// state too, so that none goes beyond 2^±30. The gradient keeps the row factor in P
+// and the products apart: its sweeps for dq and dk must make the same weights, to
+// about 2^-20 (their dot products cancel in the log decays' gradient). So does, with
+// an exponential per score, a chunk whose factors span more than 2^60 (a reset, a few
+// tokens of strong decay).
 // Q, K, V (and in the gradient the operand of the dot product) come by TMA into
 // a ring of stages, 128-byte swizzled; P is written to shared memory; S_in and
 // c ◦ V are A operands in tensor memory. Warps (20, one block an SM):
@@ -56,7 +58,7 @@ constexpr int kC = kLaChunk;
 constexpr long long kWaitClocks = 4000000000ll;  // every wait gives up after about 2 s
 constexpr int kStatusLinattnWait = 6;         // device error code
 constexpr int kThr = 640;
-constexpr float kRange = 32.f;                // |log2| a chunk's split factors may reach
+constexpr float kRange = 60.f;                // |log2| a chunk's split factors may span
 constexpr int kWarpTma = 2, kWarpMma = 3;
 constexpr int kMaps = 8;
 
@@ -264,7 +266,8 @@ template <int D, bool kBwd, bool kFull> struct Cols {
 // What is special about a chunk.
 struct __align__(8) Kind {
     unsigned char strong;  // the factors of P leave float32's comfortable range
-    unsigned char none[3];
+    unsigned char resets;  // may hold some (then it is strong)
+    unsigned char none[2];
     unsigned char odd[4];  // bit 0: V holds a value that is not finite, by 32 columns; bit 1:
                            // the row's length ends in it
 };
@@ -293,6 +296,7 @@ __device__ __forceinline__ void kept_rows(uint64_t cuts, bool rev, int *from, in
 }
 
 template <int D, bool kBwd, bool kFull> struct TcSmem {
+    static constexpr bool kCentred = kFull && !kBwd;
     static constexpr int kTiles = !kFull ? 2 : kBwd ? 4 : 3;  // (q,) k, v (, dot)
     static constexpr int kK = kFull ? 1 : 0, kV = kK + 1;     // places of k and v
     static constexpr int kStages = kFull ? 3 : 6;
@@ -305,6 +309,7 @@ template <int D, bool kBwd, bool kFull> struct TcSmem {
     float colf[kSlots][kC];         // column factors of P; in a strong chunk those of A's rounding
     float colw[kSlots][kC];
     float decay[kSlots];
+    float scale[kCentred ? kSlots : 1];  // of the state entering, 2^(the factors' middle)
     Kind kind[kSlots];
     uint64_t cuts[kSlots];          // of strong chunks; others have none
     uint64_t reached[kFull ? D : 1];  // an odd chunk's tokens that such values reach, by column
@@ -645,6 +650,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
     typedef TcSmem<D, kBwd, kFull> Smem;
     typedef Cols<D, kBwd, kFull> C;
     constexpr int kStages = Smem::kStages, kSlots = Smem::kSlots;
+    constexpr bool kCentred = Smem::kCentred;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     // 1024-byte aligned: the 128-byte swizzle pattern is taken from address bits 7..9
     Smem &S = *reinterpret_cast<Smem *>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -780,25 +786,37 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 double exact[2];
                 float A[2], row[2], colf[2], colw[2];
                 bool far = false;
+                // Forward, the factors are taken about the middle of the chunk's decay: each
+                // keeps within 2^±30 (backwards P takes both, and no more than their product).
+                float at = 0.f;
+                if (kCentred) {
+                    at = rintf(0.5f * (float)end);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        far = far || !(fabsf((float)G[e] - at) <= 0.5f * kRange);
+                    far = __any_sync(0xffffffffu, far);
+                    if (far) at = 0.f;
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     exact[e] = rev ? end - G[e] : G[e];
                     A[e] = (float)exact[e];
-                    far = far || !(fabsf(A[e]) <= kRange);
-                    row[e] = a.row_scale * ex2_approx(A[e]);
-                    colf[e] = a.col_scale * ex2_approx(-A[e]);
+                    if (!kCentred) far = far || !(fabsf(A[e]) <= kRange);
+                    row[e] = a.row_scale * ex2_approx(kCentred ? A[e] - at : A[e]);
+                    colf[e] = a.col_scale * ex2_approx(kCentred ? at - A[e] : -A[e]);
                     colw[e] = a.col_scale * ex2_approx((float)(rev ? G[e] : end - G[e]));
                 }
                 // the total too: a reset on a chunk's first token is in no A backwards
-                far = __any_sync(0xffffffffu, far || !(fabsf((float)end) <= kRange));
+                if (!kCentred) far = __any_sync(0xffffffffu, far || !(fabsf((float)end) <= kRange));
+                uint32_t cut0 = 0, cut1 = 0;
                 if (far) {
                     // A strong chunk's weights are 2^(A_row − A_col) from A as it is rounded
                     // (a step of 2^-10 behind many resets, where it passes 2^13; the
                     // difference itself is exact there) and the factors of what it lost.
                     colf[0] = ex2_approx((float)((double)A[0] - exact[0]));
                     colf[1] = ex2_approx((float)((double)A[1] - exact[1]));
-                    const uint32_t cut0 = __ballot_sync(0xffffffffu, g0 < kCutLog2),
-                                   cut1 = __ballot_sync(0xffffffffu, g1 < kCutLog2);
+                    cut0 = __ballot_sync(0xffffffffu, g0 < kCutLog2);
+                    cut1 = __ballot_sync(0xffffffffu, g1 < kCutLog2);
                     if (lane == 0) S.cuts[i % kSlots] = spread(cut0) | spread(cut1) << 1;
                 }
                 const int sl = i % kSlots;
@@ -809,7 +827,9 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 if (lane == 0) {
                     S.decay[sl] = ex2_approx((float)end);
                     *reinterpret_cast<uint2 *>(&S.kind[sl]) =
-                        make_uint2(far, len - t0 < kC && len < p.seqlen ? 0x02020202u : 0u);
+                        make_uint2(far ? 1u | (!kCentred || (cut0 | cut1) ? 256u : 0u) : 0u,
+                                   len - t0 < kC && len < p.seqlen ? 0x02020202u : 0u);
+                    if (kCentred) S.scale[sl] = ex2_approx(at);
                 }
                 seg_log2 += end;
                 arrive(&S.full[s]);
@@ -1023,7 +1043,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
             const char *tile = reinterpret_cast<const char *>(S.tile[s][Smem::kV]);
             const int sl = i % kSlots;
             const float *w = S.colw[sl];
-            const bool strong = S.kind[sl].strong != 0;
+            const bool resets = S.kind[sl].resets != 0;
             uint32_t odd = 0;  // NaN where V is not finite
             // rolled: the loop bodies of the five roles share the instruction caches. The
             // first quarter is made while U still reads the previous parts.
@@ -1066,7 +1086,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 }
             }
             if (!ok) break;
-            if (__any_sync(0xffffffffu, strong || holds_odd(odd))) {
+            if (__any_sync(0xffffffffu, resets || holds_odd(odd))) {
                 ok = odd_chunk(S, i, rev, fine, holds_odd(odd));
                 if (!ok) break;
             }
@@ -1097,16 +1117,19 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
         for (int i = 0; i < n; ++i) {
             const int buf = i % kUBufs, use = i / kUBufs;
             if (kFull) {
-                ok = wait(&S.st_empty, (i & 1) ^ 1);
+                ok = (!kCentred || wait(&S.factors[i % kSlots], i / kSlots)) &&
+                     wait(&S.st_empty, (i & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
+                const float f = kCentred ? S.scale[i % kSlots] : 1.f;
                 if (d < D) {
 #pragma unroll
                     for (int k8 = 0; k8 < kH / 8; ++k8) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float x0 = st[8 * k8 + 2 * e], x1 = st[8 * k8 + 2 * e + 1];
+                            float x0 = st[8 * k8 + 2 * e], x1 = st[8 * k8 + 2 * e + 1];
+                            if (kCentred) unpair(mul2(pair(x0, x1), pair(f, f)), x0, x1);
                             hi[e] = pack_bf16x2(x0, x1);
                             if (kBwd) lo[e] = pack_bf16x2(x0 - bf_lo(hi[e]), x1 - bf_hi(hi[e]));
                         }
@@ -1119,7 +1142,7 @@ linattn_tc_kernel(const __grid_constant__ LinattnParams p, const __grid_constant
                 tc_fence_before();
                 arrive(&S.st_full);
             }
-            ok = wait(&S.factors[i % kSlots], i / kSlots) && wait(&S.u_full[buf], use);
+            ok = (kCentred || wait(&S.factors[i % kSlots], i / kSlots)) && wait(&S.u_full[buf], use);
             if (!ok) break;
             tc_fence_after();
             const float dec = S.decay[i % kSlots];

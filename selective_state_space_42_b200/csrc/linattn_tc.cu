@@ -37,11 +37,11 @@
 // there c ◦ V has three parts too, the third in the scores' columns.
 //
 // Bound: a chunk's chain of scores, P, output product and store, and of c ◦ V, U and
-// state: 2.7 µs a chunk at D = 128 (3.5 in the gradient, 1.7 in the pass over states)
-// where the MMAs alone take 0.9; 2 × 4096 tokens of 32 heads of 128: 121 µs (1786 on
-// the CUDA cores), 65536 tokens of 16 heads 467 µs. Chunks of 128 tokens would double
-// the work on P, the largest of the roles' shares. The full passes at D = 128 spill 160
-// to 190 bytes a thread at their 96 registers.
+// state: 2.6 µs a chunk at D = 128 (3.5 in the gradient, 1.7 in the pass over states)
+// where the MMAs alone take 0.9; 2 × 4096 tokens of 32 heads of 128: 118 µs (1786 on
+// the CUDA cores), 65536 tokens of 16 heads 460 µs. Chunks of 128 tokens would double
+// the work on P, the largest of the roles' shares. The forward full pass at D = 128 keeps
+// 76 bytes a thread in local memory beside its 96 registers.
 #include "linattn_params.cuh"
 #include "umma_util.cuh"
 

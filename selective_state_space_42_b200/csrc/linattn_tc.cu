@@ -266,7 +266,7 @@ template <int D, bool kBwd, bool kFull> struct Cols {
 // What is special about a chunk.
 struct __align__(8) Kind {
     unsigned char strong;  // the factors of P leave float32's comfortable range
-    unsigned char resets;  // may hold some (then it is strong)
+    unsigned char resets;  // may hold some: it is strong and (forward) does
     unsigned char none[2];
     unsigned char odd[4];  // bit 0: V holds a value that is not finite, by 32 columns; bit 1:
                            // the row's length ends in it
@@ -510,8 +510,8 @@ __device__ __forceinline__ void cv_parts(const char *tile, const float *w, int t
     }
 }
 
-// The end of c ◦ V for a strong chunk or, by every warp that meets one in V, with values
-// that are not finite. False where a wait gave up.
+// The end of c ◦ V for a chunk that may hold resets or, by every warp that meets one in
+// V, values that are not finite. False where a wait gave up.
 //   K: rows that the state leaving does not take are cleared where they hold such a
 //     value, once the chunk's scores have been made of them. The 128 threads of c ◦ V
 //     share the rows.

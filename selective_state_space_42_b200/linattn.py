@@ -102,6 +102,11 @@ def _operands(q, k, v, log_decay, initial_state, seqlens):
     return (B, L, Hq, H, dk, dv), code, (qp, kp, vp), opts
 
 
+def _scale(scale, dk):
+    """The given scale or dk^−1/2 (a dk of zero is refused with the other sizes)."""
+    return float(scale) if scale is not None else dk ** -0.5 if dk else 1.0
+
+
 def _decays(log_decay, shape, heads, dtype, device):
     """The pair of pointers (decays per token, decays per head)."""
     if log_decay is None:
@@ -130,7 +135,7 @@ def selscan_linattn_fwd(q, k, v, log_decay=None, scale=None, initial_state=None,
     sizes, code, ptrs, opts = _operands(q, k, v, log_decay, initial_state, seqlens)
     B, L, Hq, H, dk, dv = sizes
     dev = q.device
-    scale = dk ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, dk)
     with _on(dev, stream, (q, k, v, log_decay, initial_state, seqlens, y, final_state)):
         if y is None:
             y = torch.empty_like(v, memory_format=torch.contiguous_format)
@@ -159,7 +164,7 @@ def selscan_linattn_bwd(q, k, v, log_decay=None, scale=None, initial_state=None,
     sizes, code, ptrs, opts = _operands(q, k, v, log_decay, initial_state, seqlens)
     B, L, Hq, H, dk, dv = sizes
     dev, dt = q.device, q.dtype
-    scale = dk ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, dk)
     with _on(dev, stream, (q, k, v, log_decay, initial_state, seqlens, dy, dfinal_state)):
         out = dict(
             dq=torch.empty(B, L, Hq, dk, device=dev, dtype=dt),
@@ -196,7 +201,7 @@ def selscan_linattn_step(state, q, k, v, log_decay=None, scale=None, y=None, str
     Hq = q.shape[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q)
-    scale = dk ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, dk)
     per_token, per_head = _decays(log_decay, (B, H), H, dt, dev)
     with _on(dev, stream, (state, q, k, v, log_decay, y)):
         if y is None:

@@ -22,6 +22,18 @@ def test_empty_decays_have_an_empty_gradient(dtype, shape):
     assert ss.selscan_linattn_bwd(z, z, z, torch.zeros(3, device=DEV), dy=z)["dlog_decay"] is None
 
 
+def test_heads_without_columns_are_refused():
+    """dk or dv of zero: the library's own error, from every entry point."""
+    for dk, dv in ((0, 8), (8, 0)):
+        q, v = torch.zeros(1, 4, 2, dk, device=DEV), torch.zeros(1, 4, 2, dv, device=DEV)
+        with pytest.raises(ss.SelscanError):
+            ss.selscan_linattn_fwd(q, q, v)
+        with pytest.raises(ss.SelscanError):
+            ss.selscan_linattn_bwd(q, q, v, dy=v)
+        with pytest.raises(ss.SelscanError):
+            ss.selscan_linattn_step(torch.zeros(1, 2, dk, dv, device=DEV), q[:, 0], q[:, 0], v[:, 0])
+
+
 @pytest.mark.parametrize("op", ["y", "dq"])
 def test_weights_behind_many_resets(op):
     """Tokens 45 .. 63 of a chunk whose first 45 all reset, against the same tokens
